@@ -92,6 +92,16 @@ static int check_desc(const kvq_cache_desc* d) {
   return KVQ_OK;
 }
 
+// Scoring options (NULL: none).
+static int check_score(const kvq_score_desc* sc) {
+  if (sc == nullptr) return KVQ_OK;
+  if (!std::isfinite(sc->softcap) || sc->softcap < 0.f || sc->window < 0) return KVQ_ERR_INVALID_ARG;
+  if ((sc->alibi && !aligned4(sc->alibi)) || (sc->first_pos && !aligned4(sc->first_pos)) ||
+      (sc->prefix_lens && !aligned4(sc->prefix_lens)))
+    return KVQ_ERR_MISALIGNED;
+  return KVQ_OK;
+}
+
 }  // namespace kvq
 
 using namespace kvq;
@@ -187,6 +197,47 @@ int kvq_decode_step(const kvq_cache_desc* desc, int32_t num_seqs, int32_t num_q_
   return decode_launch(*desc, num_seqs, num_q_heads, q, seq_lens, max_seq_len, block_table,
                        bt_stride, sm_scale, k_codes, k_params, v_codes, v_params, out, workspace,
                        workspace_bytes, err_flags, static_cast<cudaStream_t>(stream), &rows);
+}
+
+size_t kvq_prefill_workspace_bytes(const kvq_cache_desc* desc, int32_t num_seqs,
+                                   int32_t num_q_heads, int32_t num_tokens, int32_t max_q_len,
+                                   int32_t max_seq_len) {
+  if (check_desc(desc) != KVQ_OK || num_seqs < 1 || num_q_heads < 1 || num_tokens < 0 ||
+      max_q_len < 1 || max_seq_len < 0 || num_q_heads % desc->num_kv_heads != 0 ||
+      desc->head_dim == 64 || desc->format != KVQ_FMT_INT4)
+    return 0;
+  return prefill_plan(*desc, num_seqs, num_q_heads, num_tokens, max_q_len, max_seq_len).workspace;
+}
+
+int kvq_paged_prefill_attn(const kvq_cache_desc* desc, int32_t num_seqs, int32_t num_q_heads,
+                           int32_t num_tokens, const void* q, int64_t q_stride,
+                           const int32_t* q_start, int32_t max_q_len, const int32_t* seq_lens,
+                           int32_t max_seq_len, const int32_t* block_table, int32_t bt_stride,
+                           float sm_scale, const kvq_score_desc* score, const uint8_t* k_codes,
+                           const void* k_params, const uint8_t* v_codes, const void* v_params,
+                           void* out, void* workspace, size_t workspace_bytes,
+                           int32_t* err_flags, void* stream) {
+  int st = check_desc(desc);
+  if (st == KVQ_OK) st = check_score(score);
+  if (st != KVQ_OK) return st;
+  if (num_seqs < 1 || num_q_heads < 1 || num_tokens < 0 || max_q_len < 1 || max_seq_len < 0 ||
+      bt_stride < 1 || !std::isfinite(sm_scale) || num_q_heads % desc->num_kv_heads != 0)
+    return KVQ_ERR_INVALID_ARG;
+  if (desc->head_dim == 64 || desc->format != KVQ_FMT_INT4) return KVQ_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return KVQ_OK;
+  if (!q || !q_start || !seq_lens || !block_table || !k_codes || !k_params || !v_codes ||
+      !v_params || !out)
+    return KVQ_ERR_INVALID_ARG;
+  if (q_stride < (int64_t)num_q_heads * desc->head_dim) return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(q) || q_stride % 8 != 0 || !aligned16(out) || !aligned16(k_codes) ||
+      !aligned16(v_codes) || !aligned16(k_params) || !aligned16(v_params) || !aligned4(q_start) ||
+      !aligned4(seq_lens) || !aligned4(block_table) || (err_flags && !aligned4(err_flags)))
+    return KVQ_ERR_MISALIGNED;
+  if (workspace && !aligned16(workspace)) return KVQ_ERR_MISALIGNED;
+  return prefill_launch(*desc, num_seqs, num_q_heads, num_tokens, q, q_stride, q_start, max_q_len,
+                        seq_lens, max_seq_len, block_table, bt_stride, sm_scale, score, k_codes,
+                        k_params, v_codes, v_params, out, workspace, workspace_bytes, err_flags,
+                        static_cast<cudaStream_t>(stream));
 }
 
 size_t kvq_decode_fp16_workspace_bytes(const kvq_cache_desc* desc, int32_t num_seqs,

@@ -905,50 +905,6 @@ struct MergeArgs {
   float* out;         // [S][Hq][D]
 };
 
-// R^-1 of a row held as CPL consecutive channels per lane over the 32 lanes
-// (the inverse of the block Hadamard rotation is the rotation itself, after
-// it the sign flip when there is one; the quaternion maps are inverted block
-// by block). Binary32, not part of the
-// bit-exact quantize path.
-template <int CPL>
-__device__ __forceinline__ void row_unrotate(float (&x)[CPL], int lane, int rot_kind, int lgb,
-                                             const float* quat) {
-  if (rot_kind == KVQ_ROT_HADAMARD || rot_kind == KVQ_ROT_HADAMARD_SIGNED) {
-    const int b = 1 << lgb;
-#pragma unroll
-    for (int dd = 1; dd < CPL; dd <<= 1) {
-      if (dd >= b) break;
-#pragma unroll
-      for (int i = 0; i < CPL; ++i) {
-        if ((i & dd) == 0) {
-          const float p = x[i], q = x[i + dd];
-          x[i] = p + q;
-          x[i + dd] = p - q;
-        }
-      }
-    }
-    for (int m = 1; m * CPL < b; m <<= 1) {
-      const bool lower = (lane & m) == 0;
-#pragma unroll
-      for (int i = 0; i < CPL; ++i) {
-        const float o = __shfl_xor_sync(0xffffffffu, x[i], m);
-        x[i] = lower ? x[i] + o : o - x[i];
-      }
-    }
-    const float cb = hadamard_scale(lgb);
-#pragma unroll
-    for (int i = 0; i < CPL; ++i) x[i] *= cb;
-    // R = H S with the sign diagonal S: R^-1 = S H
-    if (rot_kind == KVQ_ROT_HADAMARD_SIGNED) sign_regs<CPL>(x, quat + lane * CPL);
-  } else if (rot_kind == KVQ_ROT_QUAT) {
-    quat_inv_regs<CPL>(x, quat, lane * CPL);
-  } else if (rot_kind == KVQ_ROT_QUAT_FAST) {
-    quat_fast_inv_regs<CPL>(x, quat, lane * CPL);
-  } else if (rot_kind == KVQ_ROT_QUAT_MAT) {
-    quat_mat_fly_regs<CPL, true>(x, quat, lane * CPL);
-  }
-}
-
 template <int D>
 __global__ void __launch_bounds__(kDecWarps * kWarp) decode_merge_kernel(const MergeArgs m) {
   constexpr int CPL = D / 32;              // channels per lane

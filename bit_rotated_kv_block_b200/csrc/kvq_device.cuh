@@ -173,6 +173,10 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t by
                "r"(bytes)
                : "memory");
 }
+// One arrival without a byte count (release ordering within the CTA).
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 // true once the phase with the given parity has completed; false on timeout
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
   const uint32_t addr = smem_u32(bar);
@@ -314,6 +318,21 @@ __device__ __forceinline__ uint32_t e2m1x2_to_h2(uint32_t byte) {
       "cvt.rn.f16x2.e2m1x2 %0, t;\n\t}"
       : "=r"(r)
       : "r"(byte));
+  return r;
+}
+
+// The same selection of a word's nibbles with no centring: the half2 of the
+// codes c themselves (1024 + c - 1024, or (1024 + 16 c) / 16 - 64; exact).
+__device__ __forceinline__ uint32_t nib_c0(uint32_t z, uint32_t mask, int high) {
+  uint32_t t;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(t) : "r"(z), "r"(mask), "r"(0x64006400u));
+  return high ? h2_as_u32(__hfma2(u32_as_h2(t), u32_as_h2(0x2C002C00u), u32_as_h2(0xD400D400u)))
+              : h2_as_u32(__hsub2(u32_as_h2(t), u32_as_h2(0x64006400u)));
+}
+
+__device__ __forceinline__ float fast_rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 

@@ -107,4 +107,21 @@ int decode_fp16_launch(const kvq_cache_desc& d, int32_t S, int32_t Hq, const voi
                        const void* v_pages, float* out, void* workspace, size_t workspace_bytes,
                        int32_t* err, cudaStream_t st);
 
+// Attention of many query rows (prompt chunks; the shared prefix of a batch).
+struct PrefillPlan {
+  int64_t mtiles;    // row tiles per (sequence, KV head)
+  int splits;        // splits of the key tiles
+  int64_t ctas;
+  size_t workspace;  // bytes of partial results (0: none)
+};
+PrefillPlan prefill_plan(const kvq_cache_desc& d, int32_t S, int32_t Hq, int32_t T, int32_t max_q,
+                         int32_t max_seq_len);
+int prefill_launch(const kvq_cache_desc& d, int32_t S, int32_t Hq, int32_t T, const void* q,
+                   int64_t q_stride, const int32_t* q_start, int32_t max_q,
+                   const int32_t* seq_lens, int32_t max_seq_len, const int32_t* block_table,
+                   int32_t bt_stride, float sm_scale, const kvq_score_desc* sc,
+                   const uint8_t* k_codes, const void* k_params, const uint8_t* v_codes,
+                   const void* v_params, void* out, void* workspace, size_t workspace_bytes,
+                   int32_t* err, cudaStream_t st);
+
 }  // namespace kvq

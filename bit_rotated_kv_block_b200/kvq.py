@@ -36,6 +36,10 @@ SIGNATURES = {
                                                      _P, _P, _P, _P, _P, _P, _P]),
     "kvq_decode_step": (ctypes.c_int, [_P, _I32, _I32, _P, _P, _P, _I64, _P, _I32, _P, _I32, _F32,
                                        _P, _P, _P, _P, _P, _P, _SZ, _P, _P]),
+    "kvq_prefill_workspace_bytes": (_SZ, [_P, _I32, _I32, _I32, _I32, _I32]),
+    "kvq_paged_prefill_attn": (ctypes.c_int, [_P, _I32, _I32, _I32, _P, _I64, _P, _I32, _P, _I32,
+                                              _P, _I32, _F32, _P, _P, _P, _P, _P, _P, _P, _SZ, _P,
+                                              _P]),
     "kvq_decode_fp16_workspace_bytes": (_SZ, [_P, _I32, _I32, _I32]),
     "kvq_paged_decode_attn_fp16": (ctypes.c_int, [_P, _I32, _I32, _P, _P, _I32, _P, _I32, _F32,
                                                   _P, _P, _P, _P, _SZ, _P, _P]),
@@ -58,6 +62,13 @@ class CacheDesc(ctypes.Structure):
                 ("quat", ctypes.c_void_p), ("rope", ctypes.c_void_p),
                 ("rope_max_pos", ctypes.c_int32), ("format", ctypes.c_int32),
                 ("levels", ctypes.c_void_p)]
+
+
+class ScoreDesc(ctypes.Structure):
+    """Mirror of ``kvq_score_desc``."""
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32),
+                ("alibi", ctypes.c_void_p), ("first_pos", ctypes.c_void_p),
+                ("prefix_lens", ctypes.c_void_p)]
 
 
 _lib = None
@@ -141,6 +152,26 @@ class Cache:
         return codes, params
 
 
+class Score:
+    """Scoring options: ``softcap`` (0: none), ``window`` (0: none), ``alibi``
+    float32 CUDA [num_q_heads] of slopes, ``first_pos`` int32 CUDA with one
+    entry per query token, ``prefix_lens`` int32 CUDA [num_seqs] (prompt
+    attention only). The tensors are kept alive here."""
+
+    def __init__(self, softcap=0.0, window=0, alibi=None, first_pos=None, prefix_lens=None):
+        for t, dt, name in ((alibi, torch.float32, "alibi"), (first_pos, torch.int32, "first_pos"),
+                            (prefix_lens, torch.int32, "prefix_lens")):
+            if t is not None and (t.dtype != dt or not t.is_contiguous()):
+                raise ValueError(f"{name} must be a contiguous {dt} tensor")
+        self.alibi, self.first_pos, self.prefix_lens = alibi, first_pos, prefix_lens
+        self.desc = ScoreDesc(softcap, window, *(None if t is None else t.data_ptr()
+                                                 for t in (alibi, first_pos, prefix_lens)))
+
+
+def _score(score):
+    return None if score is None else ctypes.byref(score.desc)
+
+
 def quantize_append(cache, k, v, token_seq, token_pos, block_table, k_codes, k_params, v_codes,
                     v_params, err=None, stream=None, tok_stride=None):
     """k, v: float16 CUDA [T][H][d] (token stride ``tok_stride`` elements)."""
@@ -210,6 +241,42 @@ def decode_step(cache, q, k_new, v_new, seq_lens, max_seq_len, block_table, k_co
                                workspace.numel() * workspace.element_size(), _ptr(err),
                                _stream(stream))
     _check("kvq_decode_step", st)
+    return out
+
+
+def prefill_workspace_bytes(cache, num_seqs, num_q_heads, num_tokens, max_q_len, max_seq_len):
+    return int(lib().kvq_prefill_workspace_bytes(ctypes.byref(cache.desc), num_seqs, num_q_heads,
+                                                 num_tokens, max_q_len, max_seq_len))
+
+
+def paged_prefill_attn(cache, q, q_start, max_q_len, seq_lens, max_seq_len, block_table, k_codes,
+                       k_params, v_codes, v_params, out=None, workspace=None, sm_scale=None,
+                       score=None, err=None, stream=None):
+    """Attention of several query tokens per sequence over the cached pages
+    (which already hold their K and V). q: float16 CUDA [T][Hq][d] (any token
+    stride); ``q_start`` int32 [S + 1]: sequence s owns tokens
+    [q_start[s], q_start[s + 1]), its last positions; returns float16
+    [T][Hq][d]. ``score``: a ``Score`` (None: plain causal)."""
+    T, Hq, d = q.shape
+    S = int(seq_lens.numel())
+    if q.stride(2) != 1 or q.stride(1) != d:
+        raise ValueError("q rows of a token must be contiguous")
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.empty((T, Hq, d), dtype=torch.float16, device=q.device)
+    if workspace is None:
+        need = prefill_workspace_bytes(cache, S, Hq, T, max_q_len, max_seq_len)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    st = lib().kvq_paged_prefill_attn(ctypes.byref(cache.desc), S, Hq, T, _ptr(q),
+                                      int(q.stride(0)), _ptr(q_start), int(max_q_len),
+                                      _ptr(seq_lens), int(max_seq_len), _ptr(block_table),
+                                      int(block_table.shape[1]), float(sm_scale), _score(score),
+                                      _ptr(k_codes), _ptr(k_params), _ptr(v_codes),
+                                      _ptr(v_params), _ptr(out), _ptr(workspace),
+                                      workspace.numel() * workspace.element_size(), _ptr(err),
+                                      _stream(stream))
+    _check("kvq_paged_prefill_attn", st)
     return out
 
 

@@ -175,6 +175,31 @@ typedef struct {
   const float* levels;
 } kvq_cache_desc;
 
+/* Scoring options of the attention entry points that take one (a host struct;
+ * NULL stands for all fields zero: the plain causal scores). For query head g
+ * of a query token t at position p of its sequence (L cached tokens):
+ *   z_j = sm_scale * qhat . khat_j
+ *   z_j <- softcap * tanh(z_j / softcap)      (softcap > 0)
+ *   z_j <- z_j - alibi[g] * |p - j|           (alibi != NULL)
+ * and position j is seen if j < L, (j <= p or j < prefix_lens[s]),
+ * j > p - window (window > 0) and j >= first_pos[t]; a query that sees
+ * nothing has the output 0.
+ *  softcap      bound of the scores' magnitude, finite and >= 0; 0: none.
+ *  window       positions a query sees, its own included, >= 0; 0: all.
+ *  alibi        device float [num_q_heads], finite slopes, or NULL.
+ *  first_pos    device int32, one per query token, or NULL: the start of the
+ *               token's document in a cache that packs several.
+ *  prefix_lens  device int32 [num_seqs], or NULL: positions below it are seen
+ *               by every query of the sequence, earlier ones too (prompt
+ *               attention only: a decode query sees no later position). */
+typedef struct {
+  float softcap;
+  int32_t window;
+  const float* alibi;
+  const int32_t* first_pos;
+  const int32_t* prefix_lens;
+} kvq_score_desc;
+
 /*
  * kvq_quantize_append -- rotate, quantize, pack and scatter new tokens of K
  * and V into the INT4 pools ("SAW-INT4", Summary/Method: the fused
@@ -296,6 +321,50 @@ int kvq_decode_step(const kvq_cache_desc* desc, int32_t num_seqs, int32_t num_q_
                     int32_t bt_stride, float sm_scale, uint8_t* k_codes, void* k_params,
                     uint8_t* v_codes, void* v_params, float* out, void* workspace,
                     size_t workspace_bytes, int32_t* err_flags, void* stream);
+
+/*
+ * kvq_paged_prefill_attn -- attention of several query tokens per sequence (a
+ * prompt, a chunk of one, or a few guessed tokens to check) over the cached
+ * pages, which already hold the K and V of those tokens (kvq_quantize_append
+ * first). The pages' method reads the INT4 cache in decode; this is the same
+ * attention for the prompt phase of the same serving stack.
+ *
+ *  num_tokens   T >= 0: query tokens of the call (0 is a no-op).
+ *  q            binary16 [T][Hq][d], not rotated; token t's rows start at
+ *               element t * q_stride. 16-byte aligned.
+ *  q_stride     elements between consecutive tokens, >= Hq * d, multiple of 8.
+ *  q_start      device int32 [num_seqs + 1], ascending: the tokens of
+ *               sequence s are rows [q_start[s], q_start[s + 1]) and are the
+ *               last ones of the sequence, at positions seq_lens[s] - n + i.
+ *  max_q_len    upper bound of the tokens of one sequence (>= 1).
+ *  seq_lens     device int32 [num_seqs], cached tokens INCLUDING the query's.
+ *  score        scoring options, a host pointer (NULL: plain causal).
+ *  out          binary16 [T][Hq][d], original basis. Rows at and past
+ *               q_start[num_seqs] are not written.
+ *  workspace    >= kvq_prefill_workspace_bytes(...) bytes, 16-byte aligned
+ *               (may be NULL where that is 0); no initialisation. Calls that
+ *               share a workspace must not overlap in time.
+ * Supported: KVQ_FMT_INT4, head_dim 128 and 256, every rotation and RoPE
+ * (query t is turned by its own position), any Hq that is a multiple of H.
+ * A range of q_start that is not inside [0, T] or longer than max_q_len sets
+ * KVQ_ERRF_SEQ, its rows are not written; a length < n, > max_seq_len or past
+ * the table sets KVQ_ERRF_LEN, its rows are 0; tokens of a bad page
+ * (KVQ_ERRF_PAGE) are not seen.
+ * Accuracy: weights p and the dequantized values enter the product as
+ * binary16 (one rounding each), the query with about 22 bits and the key
+ * codes exactly, all sums binary32; the result is rounded to binary16 once.
+ */
+size_t kvq_prefill_workspace_bytes(const kvq_cache_desc* desc, int32_t num_seqs,
+                                   int32_t num_q_heads, int32_t num_tokens, int32_t max_q_len,
+                                   int32_t max_seq_len);
+int kvq_paged_prefill_attn(const kvq_cache_desc* desc, int32_t num_seqs, int32_t num_q_heads,
+                           int32_t num_tokens, const void* q, int64_t q_stride,
+                           const int32_t* q_start, int32_t max_q_len, const int32_t* seq_lens,
+                           int32_t max_seq_len, const int32_t* block_table, int32_t bt_stride,
+                           float sm_scale, const kvq_score_desc* score, const uint8_t* k_codes,
+                           const void* k_params, const uint8_t* v_codes, const void* v_params,
+                           void* out, void* workspace, size_t workspace_bytes,
+                           int32_t* err_flags, void* stream);
 
 /*
  * Full-precision baseline: decode attention over an UNQUANTIZED binary16
