@@ -240,6 +240,84 @@ int kvq_paged_prefill_attn(const kvq_cache_desc* desc, int32_t num_seqs, int32_t
                         static_cast<cudaStream_t>(stream));
 }
 
+// Checks shared by the two decode forms with scoring options.
+static int check_scored(const kvq_cache_desc* desc, int32_t num_seqs, int32_t num_q_heads,
+                        const void* q, const int32_t* seq_lens, int32_t max_seq_len,
+                        const int32_t* block_table, int32_t bt_stride, float sm_scale,
+                        const kvq_score_desc* score, const uint8_t* k_codes, const void* k_params,
+                        const uint8_t* v_codes, const void* v_params, const void* out,
+                        const void* workspace, const int32_t* err_flags) {
+  int st = check_desc(desc);
+  if (st == KVQ_OK) st = check_score(score);
+  if (st != KVQ_OK) return st;
+  if (num_seqs < 1 || num_q_heads < 1 || max_seq_len < 0 || bt_stride < 1 ||
+      !std::isfinite(sm_scale) || num_q_heads % desc->num_kv_heads != 0 ||
+      (score && score->prefix_lens))
+    return KVQ_ERR_INVALID_ARG;
+  const int G = num_q_heads / desc->num_kv_heads;
+  if (desc->format != KVQ_FMT_INT4 || desc->head_dim == 64 || G > 8 ||
+      (desc->head_dim == 256 && G > 4))
+    return KVQ_ERR_UNSUPPORTED;
+  if (!q || !seq_lens || !block_table || !k_codes || !k_params || !v_codes || !v_params || !out)
+    return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(k_codes) || !aligned16(v_codes) ||
+      !aligned16(k_params) || !aligned16(v_params) || !aligned4(seq_lens) ||
+      !aligned4(block_table) || (err_flags && !aligned4(err_flags)))
+    return KVQ_ERR_MISALIGNED;
+  if (workspace && !aligned16(workspace)) return KVQ_ERR_MISALIGNED;
+  return KVQ_OK;
+}
+
+int kvq_paged_decode_attn_scored(const kvq_cache_desc* desc, int32_t num_seqs,
+                                 int32_t num_q_heads, const void* q, const int32_t* seq_lens,
+                                 int32_t max_seq_len, const int32_t* block_table,
+                                 int32_t bt_stride, float sm_scale, const kvq_score_desc* score,
+                                 const uint8_t* k_codes, const void* k_params,
+                                 const uint8_t* v_codes, const void* v_params, float* out,
+                                 void* workspace, size_t workspace_bytes, int32_t* err_flags,
+                                 void* stream) {
+  const int st = check_scored(desc, num_seqs, num_q_heads, q, seq_lens, max_seq_len, block_table,
+                              bt_stride, sm_scale, score, k_codes, k_params, v_codes, v_params,
+                              out, workspace, err_flags);
+  if (st != KVQ_OK) return st;
+  return decode_scored_launch(*desc, num_seqs, num_q_heads, q, seq_lens, max_seq_len, block_table,
+                              bt_stride, sm_scale, score, k_codes, k_params, v_codes, v_params,
+                              out, workspace, workspace_bytes, err_flags,
+                              static_cast<cudaStream_t>(stream));
+}
+
+size_t kvq_shared_prefix_workspace_bytes(const kvq_cache_desc* desc, int32_t num_seqs,
+                                         int32_t num_q_heads, int32_t prefix_len,
+                                         int32_t max_seq_len) {
+  if (check_desc(desc) != KVQ_OK || num_seqs < 1 || num_q_heads < 1 || prefix_len < 0 ||
+      max_seq_len < 0 || num_q_heads % desc->num_kv_heads != 0 || desc->head_dim == 64 ||
+      desc->format != KVQ_FMT_INT4)
+    return 0;
+  return shared_plan(*desc, num_seqs, num_q_heads, prefix_len, max_seq_len).workspace;
+}
+
+int kvq_shared_prefix_decode_attn(const kvq_cache_desc* desc, int32_t num_seqs,
+                                  int32_t num_q_heads, const void* q, int32_t prefix_len,
+                                  const int32_t* seq_lens, int32_t max_seq_len,
+                                  const int32_t* block_table, int32_t bt_stride, float sm_scale,
+                                  const kvq_score_desc* score, const uint8_t* k_codes,
+                                  const void* k_params, const uint8_t* v_codes,
+                                  const void* v_params, void* out, void* workspace,
+                                  size_t workspace_bytes, int32_t* err_flags, void* stream) {
+  const int st = check_scored(desc, num_seqs, num_q_heads, q, seq_lens, max_seq_len, block_table,
+                              bt_stride, sm_scale, score, k_codes, k_params, v_codes, v_params,
+                              out, workspace, err_flags);
+  if (st != KVQ_OK) return st;
+  // the prefix's pages come from one table row: they have to fit in it
+  if (prefix_len < 0 ||
+      ((int64_t)prefix_len + desc->page_size - 1) / desc->page_size > bt_stride)
+    return KVQ_ERR_INVALID_ARG;
+  return shared_launch(*desc, num_seqs, num_q_heads, q, prefix_len, seq_lens, max_seq_len,
+                       block_table, bt_stride, sm_scale, score, k_codes, k_params, v_codes,
+                       v_params, out, workspace, workspace_bytes, err_flags,
+                       static_cast<cudaStream_t>(stream));
+}
+
 size_t kvq_decode_fp16_workspace_bytes(const kvq_cache_desc* desc, int32_t num_seqs,
                                        int32_t num_q_heads, int32_t max_seq_len) {
   if (check_desc(desc) != KVQ_OK || num_seqs < 1 || num_q_heads < 1 || max_seq_len < 0 ||

@@ -90,7 +90,26 @@ struct DecodeArgs {
   uint32_t* k_params_w;
   uint8_t* v_codes_w;
   uint32_t* v_params_w;
+  // scored instantiations only
+  float capk, cap2;  // 2 / cap and cap log2(e) (0: no cap)
+  int window;        // positions seen, the query's included (0: all)
+  int skip;          // positions below are left out (a prefix attended elsewhere)
+  const float* alibi;
+  const int32_t* first_pos;
 };
+
+// cap tanh(z / cap) in base-2 units for z2 = z log2(e): near zero by the odd
+// series (to x^9: relative error below 2^-24 for |x| <= 1/4), where
+// 1 - 2 / (1 + e^2x) would cancel.
+__device__ __forceinline__ float cap_score(float z2, float capk, float cap2) {
+  const float y = z2 * capk;  // 2 x log2(e)
+  const float x = y * 0.34657359027997264f;
+  const float x2 = x * x;
+  const float ser = x * fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, 0.0218694885f, -0.0539682540f),
+                                               0.1333333333f), -0.3333333333f), 1.f);
+  const float t = fabsf(x) <= 0.25f ? ser : fmaf(-2.f, fast_rcp(1.f + fast_exp2(y)), 1.f);
+  return t * cap2;
+}
 
 // The new token of one (sequence, KV head) (position L - 1), quantized by
 // one warp exactly as kvq_quantize_append would: this lane's code bytes of
@@ -197,7 +216,9 @@ struct DecCfg {
 // spare) and most page groups skip the cross-lane maximum and the rescale.
 constexpr float kMaxSlack = 8.f;
 
-template <int D, int P, int GP>
+// SC: the scored form (cap, distance bias, and the interval [lo, L) of
+// positions that the window, the document and a skipped prefix leave).
+template <int D, int P, int GP, bool SC = false>
 __global__ void __launch_bounds__(kDecWarps * kWarp, D == 256 ? 2 : 3)
     decode_split_kernel(const DecodeArgs a) {
   static_assert(D == 128 || D == 256, "decode attention supports head_dim 128 and 256");
@@ -245,11 +266,20 @@ __global__ void __launch_bounds__(kDecWarps * kWarp, D == 256 ? 2 : 3)
   }
   bool len_ok = L >= 0 && L <= a.max_seq_len && (L + a.P - 1) / a.P <= a.bt_stride &&
                 (a.rope == nullptr || L <= a.rope_max_pos);
+  if (SC) len_ok = len_ok && (L == 0 || L >= a.skip);
   if (!len_ok) {
     if (lane == 0 && h == 0 && split == 0) raise_flag(a.err, KVQ_ERRF_LEN);
     L = 0;
   }
   const int npages = (L + P - 1) / P;
+  int lo_tok = 0;  // first position seen
+  if (SC) {
+    lo_tok = a.skip;
+    if (a.window > 0 && L > a.window) lo_tok = max(lo_tok, L - a.window);
+    if (a.first_pos != nullptr) lo_tok = max(lo_tok, a.first_pos[s]);
+    lo_tok = min(lo_tok, L);
+  }
+  const int lo_pg = SC ? (lo_tok < L ? lo_tok / P : npages) : 0;  // pages before it are not read
   // this warp's pages: a contiguous range; the sequence's pages are dealt
   // out evenly over its splits (range sizes differ by at most one page)
   // In a fused step the last split also quantizes the new token first: it
@@ -261,10 +291,11 @@ __global__ void __launch_bounds__(kDecWarps * kWarp, D == 256 ? 2 : 3)
   // last split can come out empty: the split before it then holds the last
   // page and quantizes the new token (the owner is whichever split holds
   // that page), and every page is still in exactly one range.
-  const int lead = npages >= 4 * nspl ? a.lead : 0;
-  const int64_t vpages = (int64_t)npages + lead;
-  const int pg_lo = split == 0 ? 0 : (int)min((int64_t)npages, (split * vpages) / nspl);
-  const int pg_hi = split + 1 == nspl ? npages : (int)min((int64_t)npages, ((split + 1) * vpages) / nspl);
+  const int lead = !SC && npages >= 4 * nspl ? a.lead : 0;
+  const int64_t vpages = (int64_t)(npages - lo_pg) + lead;
+  const int pg_lo = split == 0 ? lo_pg : (int)min((int64_t)npages, lo_pg + (split * vpages) / nspl);
+  const int pg_hi = split + 1 == nspl ? npages
+                                      : (int)min((int64_t)npages, lo_pg + ((split + 1) * vpages) / nspl);
   const int ngrp = (pg_hi - pg_lo + C::PG - 1) / C::PG;  // stage groups
   const int32_t* const bt_row = a.block_table + (int64_t)s * a.bt_stride;
   // fused step: the warp whose range holds the page of position L - 1
@@ -273,7 +304,7 @@ __global__ void __launch_bounds__(kDecWarps * kWarp, D == 256 ? 2 : 3)
   // the staged copy of that page, so no fence or global round trip stands
   // between the write and the attention that reads it
   const int new_pg = L >= 1 ? (L - 1) / P : -1;
-  const bool step_owner = a.k_new != nullptr && new_pg >= pg_lo && new_pg < pg_hi;
+  const bool step_owner = !SC && a.k_new != nullptr && new_pg >= pg_lo && new_pg < pg_hi;
   int new_grp = -1;  // group of the new token's page (-1: none to patch)
   // its inputs go out before this warp's (and ahead of most warps') page
   // copies, so they do not queue behind the page traffic: the two binary16
@@ -459,6 +490,9 @@ __global__ void __launch_bounds__(kDecWarps * kWarp, D == 256 ? 2 : 3)
   // cancel. 128 qsum = QA * 2^16 + QB (0 <= QB < 2^16) comes off the limb
   // halves before they are combined.
   float zs, zq, zq8, zA, zB;
+  // the head's slope in base-2 units
+  const float slope2 =
+      SC && a.alibi != nullptr && head_ok ? a.alibi[g] * 1.4426950408889634f : 0.f;
   int QA, QB;
   // A fragments per k-step kk: the lane's 8 channels j*QW + 8kk + [0, 8),
   // even ones in a[0]/a[1], odd ones in a[2]/a[3]. Rows:
@@ -590,7 +624,7 @@ __global__ void __launch_bounds__(kDecWarps * kWarp, D == 256 ? 2 : 3)
     }
     const int tok0 = (pg_lo + gi * C::PG) * P;  // first token of the group
     // groups whose every token is cached skip all per-token masking
-    const bool full = all_ok && tok0 + C::PG * P <= L;
+    const bool full = all_ok && tok0 + C::PG * P <= L && (!SC || tok0 >= lo_tok);
 
     auto body = [&](auto masked_tag) {
       constexpr bool MASKED = decltype(masked_tag)::value;
@@ -659,10 +693,14 @@ __global__ void __launch_bounds__(kDecWarps * kWarp, D == 256 ? 2 : 3)
           const float zd = fmaf(fA[e], zA, fmaf(fB[e], zB, zq8));
           const uint32_t kpw = *reinterpret_cast<const uint32_t*>(st + kps[e] + pofs);
           const float2 sm = __half22float2(u32_as_h2(kpw));  // (scale, min)
-          const float sc = fmaf(sm.x, zd, sm.y * zq);
+          float sc = fmaf(sm.x, zd, sm.y * zq);
+          const int tok = tok0 + (tt / C::TILES) * P + (tt % C::TILES) * 16 + tks[e];
+          if (SC) {
+            if (a.capk > 0.f) sc = cap_score(sc, a.capk, a.cap2);
+            if (a.alibi != nullptr) sc = fmaf(slope2, (float)(tok - (L - 1)), sc);
+          }
           if (MASKED) {
-            const int tok = tok0 + (tt / C::TILES) * P + (tt % C::TILES) * 16 + tks[e];
-            z[tt][e] = tok < L ? sc : -INFINITY;
+            z[tt][e] = tok < L && (!SC || tok >= lo_tok) ? sc : -INFINITY;
           } else {
             z[tt][e] = sc;
           }
@@ -1047,9 +1085,9 @@ DecodePlan decode_plan(const kvq_cache_desc& d, int32_t S, int32_t Hq, int32_t m
   return pl;
 }
 
-template <int D, int P, int GP>
+template <int D, int P, int GP, bool SC>
 static cudaError_t launch_split(const DecodeArgs& a, cudaStream_t st) {
-  auto kern = decode_split_kernel<D, P, GP>;
+  auto kern = decode_split_kernel<D, P, GP, SC>;
   const size_t smem = split_smem<D, P, GP>();
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
@@ -1060,12 +1098,39 @@ static cudaError_t launch_split(const DecodeArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+template <bool SC>
 static cudaError_t launch_split_any(const DecodeArgs& a, int D, int GP, cudaStream_t st) {
 #define KVQ_LS(d_, p_, g_) \
-  if (D == d_ && a.P == p_ && GP == g_) return launch_split<d_, p_, g_>(a, st);
+  if (D == d_ && a.P == p_ && GP == g_) return launch_split<d_, p_, g_, SC>(a, st);
   KVQ_DECODE_CONFIGS(KVQ_LS)
 #undef KVQ_LS
   return cudaErrorInvalidValue;
+}
+
+// Arguments shared by the plain and the scored launches.
+static DecodeArgs decode_args(const kvq_cache_desc& d, const DecodePlan& pl, int32_t S, int32_t Hq,
+                              const void* q, const int32_t* seq_lens, int32_t max_seq_len,
+                              const int32_t* block_table, int32_t bt_stride, float sm_scale,
+                              const uint8_t* k_codes, const void* k_params,
+                              const uint8_t* v_codes, const void* v_params, float* out,
+                              void* workspace, int32_t* err) {
+  int lgb = 0;
+  while ((1 << lgb) < d.rot_block) ++lgb;
+  DecodeArgs a = {};
+  a.S = S; a.Hq = Hq; a.H = d.num_kv_heads; a.G = Hq / d.num_kv_heads;
+  a.P = d.page_size; a.NP = d.num_pages;
+  a.bt_stride = bt_stride; a.max_seq_len = max_seq_len; a.splits = pl.splits; a.nhi = pl.nhi;
+  a.rot_kind = d.rot_kind; a.lgb = lgb;
+  a.scale2 = (float)((double)sm_scale * 1.4426950408889634074);
+  a.q = static_cast<const __half*>(q); a.quat = d.quat;
+  a.rope = d.rope; a.rope_max_pos = d.rope_max_pos;
+  a.seq_lens = seq_lens; a.block_table = block_table;
+  a.k_codes = k_codes; a.k_params = static_cast<const uint32_t*>(k_params);
+  a.v_codes = v_codes; a.v_params = static_cast<const uint32_t*>(v_params);
+  a.out = out;
+  a.part = static_cast<float*>(workspace);
+  a.err = err;
+  return a;
 }
 
 int decode_launch(const kvq_cache_desc& d, int32_t S, int32_t Hq, const void* q,
@@ -1088,22 +1153,8 @@ int decode_launch(const kvq_cache_desc& d, int32_t S, int32_t Hq, const void* q,
   if ((D != 128 && D != 256) || (D == 256 && GP != 4)) return KVQ_ERR_UNSUPPORTED;
   const DecodePlan pl = decode_plan(d, S, Hq, max_seq_len);
   if (workspace == nullptr || workspace_bytes < pl.workspace) return KVQ_ERR_WORKSPACE;
-  int lgb = 0;
-  while ((1 << lgb) < d.rot_block) ++lgb;
-
-  DecodeArgs a;
-  a.S = S; a.Hq = Hq; a.H = d.num_kv_heads; a.G = G; a.P = d.page_size; a.NP = d.num_pages;
-  a.bt_stride = bt_stride; a.max_seq_len = max_seq_len; a.splits = pl.splits; a.nhi = pl.nhi;
-  a.rot_kind = d.rot_kind; a.lgb = lgb;
-  a.scale2 = (float)((double)sm_scale * 1.4426950408889634074);
-  a.q = static_cast<const __half*>(q); a.quat = d.quat;
-  a.rope = d.rope; a.rope_max_pos = d.rope_max_pos;
-  a.seq_lens = seq_lens; a.block_table = block_table;
-  a.k_codes = k_codes; a.k_params = static_cast<const uint32_t*>(k_params);
-  a.v_codes = v_codes; a.v_params = static_cast<const uint32_t*>(v_params);
-  a.out = out;
-  a.part = static_cast<float*>(workspace);
-  a.err = err;
+  DecodeArgs a = decode_args(d, pl, S, Hq, q, seq_lens, max_seq_len, block_table, bt_stride,
+                             sm_scale, k_codes, k_params, v_codes, v_params, out, workspace, err);
   a.lead = (128 + d.page_size - 1) / d.page_size;  // 128 tokens: measured best of 48-208
   a.k_new = step ? static_cast<const __half*>(step->k_new) : nullptr;
   a.v_new = step ? static_cast<const __half*>(step->v_new) : nullptr;
@@ -1112,10 +1163,58 @@ int decode_launch(const kvq_cache_desc& d, int32_t S, int32_t Hq, const void* q,
   a.v_codes_w = const_cast<uint8_t*>(v_codes);
   a.k_params_w = static_cast<uint32_t*>(const_cast<void*>(k_params));
   a.v_params_w = static_cast<uint32_t*>(const_cast<void*>(v_params));
-  cudaError_t e = launch_split_any(a, D, GP, st);
+  cudaError_t e = launch_split_any<false>(a, D, GP, st);
   if (e == cudaErrorInvalidValue) return KVQ_ERR_UNSUPPORTED;
   if (e != cudaSuccess) return KVQ_ERR_CUDA;
   return decode_merge_launch(d, S, Hq, pl.splits, pl.nhi, a.part, out, st);
+}
+
+DecodePlan decode_scored_plan(const kvq_cache_desc& d, int32_t S, int32_t Hq, int32_t max_seq_len,
+                              int32_t skip, const kvq_score_desc* sc) {
+  // a window or a skipped prefix bounds the positions of a split range; the
+  // splits of fewer positions are never more (the full plan's workspace fits)
+  int32_t n = max_seq_len > skip ? max_seq_len - skip : 0;
+  if (sc && sc->window > 0 && sc->window < n) n = sc->window;
+  return decode_plan(d, S, Hq, n);
+}
+
+int decode_scored_split_launch(const kvq_cache_desc& d, int32_t S, int32_t Hq, const void* q,
+                               const int32_t* seq_lens, int32_t max_seq_len,
+                               const int32_t* block_table, int32_t bt_stride, float sm_scale,
+                               const kvq_score_desc* sc, int32_t skip, const uint8_t* k_codes,
+                               const void* k_params, const uint8_t* v_codes,
+                               const void* v_params, void* workspace, int32_t* err,
+                               cudaStream_t st) {
+  const DecodePlan pl = decode_scored_plan(d, S, Hq, max_seq_len, skip, sc);
+  DecodeArgs a = decode_args(d, pl, S, Hq, q, seq_lens, max_seq_len, block_table, bt_stride,
+                             sm_scale, k_codes, k_params, v_codes, v_params, nullptr, workspace,
+                             err);
+  a.skip = skip;
+  if (sc != nullptr) {
+    a.capk = sc->softcap > 0.f ? 2.f / sc->softcap : 0.f;
+    a.cap2 = (float)((double)sc->softcap * 1.4426950408889634074);
+    a.window = sc->window;
+    a.alibi = sc->alibi;
+    a.first_pos = sc->first_pos;
+  }
+  cudaError_t e = launch_split_any<true>(a, d.head_dim, a.G <= 4 ? 4 : 8, st);
+  if (e == cudaErrorInvalidValue) return KVQ_ERR_UNSUPPORTED;
+  return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+int decode_scored_launch(const kvq_cache_desc& d, int32_t S, int32_t Hq, const void* q,
+                         const int32_t* seq_lens, int32_t max_seq_len,
+                         const int32_t* block_table, int32_t bt_stride, float sm_scale,
+                         const kvq_score_desc* sc, const uint8_t* k_codes, const void* k_params,
+                         const uint8_t* v_codes, const void* v_params, float* out,
+                         void* workspace, size_t workspace_bytes, int32_t* err, cudaStream_t st) {
+  const DecodePlan pl = decode_scored_plan(d, S, Hq, max_seq_len, 0, sc);
+  if (workspace == nullptr || workspace_bytes < pl.workspace) return KVQ_ERR_WORKSPACE;
+  const int r = decode_scored_split_launch(d, S, Hq, q, seq_lens, max_seq_len, block_table,
+                                           bt_stride, sm_scale, sc, 0, k_codes, k_params, v_codes,
+                                           v_params, workspace, err, st);
+  if (r != KVQ_OK) return r;
+  return decode_merge_launch(d, S, Hq, pl.splits, pl.nhi, static_cast<float*>(workspace), out, st);
 }
 
 int decode_merge_launch(const kvq_cache_desc& d, int32_t S, int32_t Hq, int splits, int nhi,

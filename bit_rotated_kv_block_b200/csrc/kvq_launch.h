@@ -71,6 +71,25 @@ int decode_launch(const kvq_cache_desc& d, int32_t S, int32_t Hq, const void* q,
                   float* out, void* workspace, size_t workspace_bytes, int32_t* err,
                   cudaStream_t st, const DecodeStepRows* step = nullptr);
 
+// The scored form (INT4 pages): positions from `skip` on, inside the interval
+// the options leave. The split launch alone writes the partial results
+// (layout and plan as decode_launch's); decode_scored_launch merges them too.
+DecodePlan decode_scored_plan(const kvq_cache_desc& d, int32_t S, int32_t Hq, int32_t max_seq_len,
+                              int32_t skip, const kvq_score_desc* sc);
+int decode_scored_split_launch(const kvq_cache_desc& d, int32_t S, int32_t Hq, const void* q,
+                               const int32_t* seq_lens, int32_t max_seq_len,
+                               const int32_t* block_table, int32_t bt_stride, float sm_scale,
+                               const kvq_score_desc* sc, int32_t skip, const uint8_t* k_codes,
+                               const void* k_params, const uint8_t* v_codes,
+                               const void* v_params, void* workspace, int32_t* err,
+                               cudaStream_t st);
+int decode_scored_launch(const kvq_cache_desc& d, int32_t S, int32_t Hq, const void* q,
+                         const int32_t* seq_lens, int32_t max_seq_len,
+                         const int32_t* block_table, int32_t bt_stride, float sm_scale,
+                         const kvq_score_desc* sc, const uint8_t* k_codes, const void* k_params,
+                         const uint8_t* v_codes, const void* v_params, float* out,
+                         void* workspace, size_t workspace_bytes, int32_t* err, cudaStream_t st);
+
 // The merge kernel over split partial results [S][Hq][splits][d + 4] (the
 // running sums, then the base-2 maximum and total weight), rotated back.
 // Query heads of the first `nhi` (sequence, KV head) pairs combine `splits`
@@ -123,5 +142,23 @@ int prefill_launch(const kvq_cache_desc& d, int32_t S, int32_t Hq, int32_t T, co
                    const uint8_t* k_codes, const void* k_params, const uint8_t* v_codes,
                    const void* v_params, void* out, void* workspace, size_t workspace_bytes,
                    int32_t* err, cudaStream_t st);
+
+// Decode attention of a batch whose first prefix_len positions are the same
+// pages: the prefix once for all (rows = sequences x heads of a group), then
+// each sequence's own positions, then one merge. Bytes of both parts' partial
+// results, the prefix's first.
+struct SharedPlan {
+  PrefillPlan prefix;  // splits 0: no prefix
+  DecodePlan own;
+  size_t prefix_bytes, workspace;
+};
+SharedPlan shared_plan(const kvq_cache_desc& d, int32_t S, int32_t Hq, int32_t prefix_len,
+                       int32_t max_seq_len);
+int shared_launch(const kvq_cache_desc& d, int32_t S, int32_t Hq, const void* q,
+                  int32_t prefix_len, const int32_t* seq_lens, int32_t max_seq_len,
+                  const int32_t* block_table, int32_t bt_stride, float sm_scale,
+                  const kvq_score_desc* sc, const uint8_t* k_codes, const void* k_params,
+                  const uint8_t* v_codes, const void* v_params, void* out, void* workspace,
+                  size_t workspace_bytes, int32_t* err, cudaStream_t st);
 
 }  // namespace kvq

@@ -120,7 +120,7 @@ struct PrefillArgs {
   const uint8_t* v_codes;
   const uint32_t* v_params;
   __half* out;   // [T][Hq][D] (splits == 1)
-  float* part;   // [T][Hq][splits][D + 4]
+  float* part;   // [T][Hq][splits][D + 4], or NULL: one split, out is written
   int32_t* err;
 };
 
@@ -590,7 +590,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
       }
       __syncwarp();
       // ---- the row's result (V entered halved)
-      if (a.splits > 1) {
+      if (a.part != nullptr) {
         float* dst = a.part + (R.row * a.splits + split) * (D + 4);
         const bool some = ntile > 0 && M != -INFINITY;
         if (ntile > 0) {
@@ -1013,12 +1013,56 @@ int prefill_launch(const kvq_cache_desc& d, int32_t S, int32_t Hq, int32_t T, co
   a.T = T; a.q_stride = q_stride; a.q_start = q_start; a.max_q = max_q;
   a.mtiles = (int)pl.mtiles; a.splits = pl.splits; a.shared_len = -1;
   a.out = static_cast<__half*>(out);
-  a.part = static_cast<float*>(workspace);
+  a.part = pl.splits > 1 ? static_cast<float*>(workspace) : nullptr;
   if (launch_any(a, d.head_dim, (int)pl.ctas, st) != cudaSuccess) return KVQ_ERR_CUDA;
   if (pl.splits > 1 &&
       launch_merge(d, (int64_t)T * Hq, a.G, pl.splits, 0, 0, a.part, nullptr, out, st) != cudaSuccess)
     return KVQ_ERR_CUDA;
   return KVQ_OK;
+}
+
+SharedPlan shared_plan(const kvq_cache_desc& d, int32_t S, int32_t Hq, int32_t prefix_len,
+                       int32_t max_seq_len) {
+  SharedPlan p{};
+  if (prefix_len > 0) {
+    p.prefix = plan_rows(d.head_dim, d.num_kv_heads, 1, (int64_t)S * (Hq / d.num_kv_heads),
+                         (int64_t)S * Hq, prefix_len);
+    p.prefix_bytes = (size_t)S * Hq * p.prefix.splits * (d.head_dim + 4) * sizeof(float);
+  }
+  p.own = decode_scored_plan(d, S, Hq, max_seq_len, prefix_len, nullptr);
+  p.workspace = p.prefix_bytes + p.own.workspace;
+  return p;
+}
+
+int shared_launch(const kvq_cache_desc& d, int32_t S, int32_t Hq, const void* q,
+                  int32_t prefix_len, const int32_t* seq_lens, int32_t max_seq_len,
+                  const int32_t* block_table, int32_t bt_stride, float sm_scale,
+                  const kvq_score_desc* sc, const uint8_t* k_codes, const void* k_params,
+                  const uint8_t* v_codes, const void* v_params, void* out, void* workspace,
+                  size_t workspace_bytes, int32_t* err, cudaStream_t st) {
+  const SharedPlan pl = shared_plan(d, S, Hq, prefix_len, max_seq_len);
+  if (workspace == nullptr || workspace_bytes < pl.workspace) return KVQ_ERR_WORKSPACE;
+  if (pl.prefix.ctas > INT_MAX || (int64_t)S * Hq > INT_MAX) return KVQ_ERR_UNSUPPORTED;
+  float* const pa = static_cast<float*>(workspace);
+  float* const pb = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + pl.prefix_bytes);
+  if (prefix_len > 0) {
+    PrefillArgs a;
+    fill_args(a, d, S, Hq, q, seq_lens, max_seq_len, block_table, bt_stride, sm_scale, sc, k_codes,
+              k_params, v_codes, v_params, err);
+    a.T = S; a.q_stride = (int64_t)Hq * d.head_dim; a.q_start = nullptr; a.max_q = S;
+    a.mtiles = (int)pl.prefix.mtiles; a.splits = pl.prefix.splits; a.shared_len = prefix_len;
+    a.out = nullptr;
+    a.part = pa;
+    if (launch_any(a, d.head_dim, (int)pl.prefix.ctas, st) != cudaSuccess) return KVQ_ERR_CUDA;
+  }
+  const int r = decode_scored_split_launch(d, S, Hq, q, seq_lens, max_seq_len, block_table,
+                                           bt_stride, sm_scale, sc, prefix_len, k_codes, k_params,
+                                           v_codes, v_params, pb, err, st);
+  if (r != KVQ_OK) return r;
+  // (a window shrinks the own part's plan: the launch's own counts)
+  const DecodePlan own = decode_scored_plan(d, S, Hq, max_seq_len, prefix_len, sc);
+  return launch_merge(d, (int64_t)S * Hq, Hq / d.num_kv_heads, pl.prefix.splits, own.splits,
+                      own.nhi, pa, pb, out, st) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
 }  // namespace kvq

@@ -40,6 +40,12 @@ SIGNATURES = {
     "kvq_paged_prefill_attn": (ctypes.c_int, [_P, _I32, _I32, _I32, _P, _I64, _P, _I32, _P, _I32,
                                               _P, _I32, _F32, _P, _P, _P, _P, _P, _P, _P, _SZ, _P,
                                               _P]),
+    "kvq_paged_decode_attn_scored": (ctypes.c_int, [_P, _I32, _I32, _P, _P, _I32, _P, _I32, _F32,
+                                                    _P, _P, _P, _P, _P, _P, _P, _SZ, _P, _P]),
+    "kvq_shared_prefix_workspace_bytes": (_SZ, [_P, _I32, _I32, _I32, _I32]),
+    "kvq_shared_prefix_decode_attn": (ctypes.c_int, [_P, _I32, _I32, _P, _I32, _P, _I32, _P, _I32,
+                                                     _F32, _P, _P, _P, _P, _P, _P, _P, _SZ, _P,
+                                                     _P]),
     "kvq_decode_fp16_workspace_bytes": (_SZ, [_P, _I32, _I32, _I32]),
     "kvq_paged_decode_attn_fp16": (ctypes.c_int, [_P, _I32, _I32, _P, _P, _I32, _P, _I32, _F32,
                                                   _P, _P, _P, _P, _SZ, _P, _P]),
@@ -277,6 +283,63 @@ def paged_prefill_attn(cache, q, q_start, max_q_len, seq_lens, max_seq_len, bloc
                                       workspace.numel() * workspace.element_size(), _ptr(err),
                                       _stream(stream))
     _check("kvq_paged_prefill_attn", st)
+    return out
+
+
+def paged_decode_attn_scored(cache, q, seq_lens, max_seq_len, block_table, k_codes, k_params,
+                             v_codes, v_params, score=None, out=None, workspace=None,
+                             sm_scale=None, err=None, stream=None):
+    """``paged_decode_attn`` with scoring options (a ``Score``; its first_pos
+    has one entry per sequence); same workspace."""
+    S, Hq, d = q.shape
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.empty((S, Hq, d), dtype=torch.float32, device=q.device)
+    if workspace is None:
+        need = decode_workspace_bytes(cache, S, Hq, max_seq_len)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    st = lib().kvq_paged_decode_attn_scored(ctypes.byref(cache.desc), S, Hq, _ptr(q),
+                                            _ptr(seq_lens), int(max_seq_len), _ptr(block_table),
+                                            int(block_table.shape[1]), float(sm_scale),
+                                            _score(score), _ptr(k_codes), _ptr(k_params),
+                                            _ptr(v_codes), _ptr(v_params), _ptr(out),
+                                            _ptr(workspace),
+                                            workspace.numel() * workspace.element_size(),
+                                            _ptr(err), _stream(stream))
+    _check("kvq_paged_decode_attn_scored", st)
+    return out
+
+
+def shared_prefix_workspace_bytes(cache, num_seqs, num_q_heads, prefix_len, max_seq_len):
+    return int(lib().kvq_shared_prefix_workspace_bytes(ctypes.byref(cache.desc), num_seqs,
+                                                       num_q_heads, prefix_len, max_seq_len))
+
+
+def shared_prefix_decode_attn(cache, q, prefix_len, seq_lens, max_seq_len, block_table, k_codes,
+                              k_params, v_codes, v_params, score=None, out=None, workspace=None,
+                              sm_scale=None, err=None, stream=None):
+    """Decode attention of a batch whose sequences share their first
+    ``prefix_len`` tokens (pages taken from row 0 of the table, read once for
+    the batch); ``seq_lens`` are whole lengths. q: float16 CUDA [S][Hq][d];
+    returns float16 [S][Hq][d]."""
+    S, Hq, d = q.shape
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.empty((S, Hq, d), dtype=torch.float16, device=q.device)
+    if workspace is None:
+        need = shared_prefix_workspace_bytes(cache, S, Hq, prefix_len, max_seq_len)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    st = lib().kvq_shared_prefix_decode_attn(ctypes.byref(cache.desc), S, Hq, _ptr(q),
+                                             int(prefix_len), _ptr(seq_lens), int(max_seq_len),
+                                             _ptr(block_table), int(block_table.shape[1]),
+                                             float(sm_scale), _score(score), _ptr(k_codes),
+                                             _ptr(k_params), _ptr(v_codes), _ptr(v_params),
+                                             _ptr(out), _ptr(workspace),
+                                             workspace.numel() * workspace.element_size(),
+                                             _ptr(err), _stream(stream))
+    _check("kvq_shared_prefix_decode_attn", st)
     return out
 
 

@@ -367,6 +367,61 @@ int kvq_paged_prefill_attn(const kvq_cache_desc* desc, int32_t num_seqs, int32_t
                            int32_t* err_flags, void* stream);
 
 /*
+ * kvq_paged_decode_attn_scored -- kvq_paged_decode_attn with scoring options
+ * (score, a host pointer; NULL: as kvq_paged_decode_attn): the query of
+ * sequence s is at position seq_lens[s] - 1, first_pos has one entry per
+ * sequence, prefix_lens must be NULL. Pages that lie wholly before the
+ * window or the document are not read (their table entries may be stale).
+ * INT4 pages (KVQ_FMT_INT4; others return KVQ_ERR_UNSUPPORTED); all other
+ * arguments, the workspace (kvq_decode_workspace_bytes), the accuracy, the
+ * return codes and the flags as for kvq_paged_decode_attn.
+ */
+int kvq_paged_decode_attn_scored(const kvq_cache_desc* desc, int32_t num_seqs,
+                                 int32_t num_q_heads, const void* q, const int32_t* seq_lens,
+                                 int32_t max_seq_len, const int32_t* block_table,
+                                 int32_t bt_stride, float sm_scale, const kvq_score_desc* score,
+                                 const uint8_t* k_codes, const void* k_params,
+                                 const uint8_t* v_codes, const void* v_params, float* out,
+                                 void* workspace, size_t workspace_bytes, int32_t* err_flags,
+                                 void* stream);
+
+/*
+ * kvq_shared_prefix_decode_attn -- decode attention for a batch whose
+ * sequences begin with the same prefix_len tokens: the prefix's pages are
+ * read once per KV head for the whole batch instead of once per sequence.
+ * The result is that of kvq_paged_decode_attn_scored on the same cache,
+ * rounded to binary16.
+ *
+ *  prefix_len   P0 >= 0, a host value: positions [0, P0) of every sequence
+ *               hold the same tokens; their pages are taken from row 0 of
+ *               block_table. The other rows' entries below P0 / page_size
+ *               are not read. P0 need not be a multiple of the page size:
+ *               the page that holds position P0 is each sequence's own copy,
+ *               of which the positions from P0 on are read.
+ *  seq_lens     int32 [S], whole lengths, the prefix included; 0 is an idle
+ *               slot of a padded batch (out = 0), a length in (0, P0) is
+ *               invalid (KVQ_ERRF_LEN, out = 0).
+ *  score        scoring options, a host pointer (NULL: plain), as for
+ *               kvq_paged_decode_attn_scored; prefix_lens must be NULL.
+ *  out          binary16 [S][Hq][d], original basis.
+ *  workspace    >= kvq_shared_prefix_workspace_bytes(...) bytes, 16-byte
+ *               aligned; no initialisation.
+ * Supported: KVQ_FMT_INT4 and the geometries of kvq_paged_decode_attn. The
+ * prefix part has the accuracy of kvq_paged_prefill_attn.
+ */
+size_t kvq_shared_prefix_workspace_bytes(const kvq_cache_desc* desc, int32_t num_seqs,
+                                         int32_t num_q_heads, int32_t prefix_len,
+                                         int32_t max_seq_len);
+int kvq_shared_prefix_decode_attn(const kvq_cache_desc* desc, int32_t num_seqs,
+                                  int32_t num_q_heads, const void* q, int32_t prefix_len,
+                                  const int32_t* seq_lens, int32_t max_seq_len,
+                                  const int32_t* block_table, int32_t bt_stride, float sm_scale,
+                                  const kvq_score_desc* score, const uint8_t* k_codes,
+                                  const void* k_params, const uint8_t* v_codes,
+                                  const void* v_params, void* out, void* workspace,
+                                  size_t workspace_bytes, int32_t* err_flags, void* stream);
+
+/*
  * Full-precision baseline: decode attention over an UNQUANTIZED binary16
  * paged cache, without rotation. The INT4 cache is measured against it (page
  * "SAW-INT4: System-Aware 4-Bit KV-Cache Quantization for Real-World LLM

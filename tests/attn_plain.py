@@ -116,3 +116,13 @@ def half_tolerance(out, A, S, L, vmax, cap=0.0, bias=0.0):
     d = out.shape[-1]
     return A * (2.0 ** -10 * (1 + 1 / 64) + 2.0 ** -11 + 2 * dz) \
         + math.sqrt(d) * 2.0 ** -25 + L * 2.0 ** -32 * vmax * math.sqrt(d)
+
+
+def float_tolerance(A, S, L, cap=0.0, bias=0.0):
+    """2-norm bound per output row of the binary32 decode: weights as hi + lo
+    pairs (2^-22), products of 64 tokens summed with at most 8 truncations
+    (2^-23 each), then one binary32 addition per 64 tokens and per split
+    (at most L / 64 of both together and 64 more, 2^-24 each, doubled), the
+    exponential 2^-21; scores as in half_tolerance."""
+    dz = S * 2.0 ** -20 + cap * 2.0 ** -21 + bias * 2.0 ** -22 + 2.0 ** -20
+    return A * ((L / 64 + 64) * 2.0 ** -23 + 2.0 ** -19 + 2 * dz) + 1e-30
