@@ -6,22 +6,30 @@
 // KV head's group and the tokens of a sequence (or, over a shared prefix, the
 // sequences of the batch) are the rows of one matrix product with that KV
 // head's keys. With q^ = R q, codes c, row scale s and minimum m of a key,
-//   z_j = sm_scale (s_j sum_i (c_ji - 8) q^_i + (m_j + 8 s_j) sum_i q^_i),
+//   z_j = sm_scale (s_j sum_i (64 + c_ji) q^_i + (m_j - 64 s_j) sum_i q^_i),
 // then the cap, the distance bias and the interval mask [lo, hi) of the row,
 // and out = R^-1 sum_j p_j v^_j with the online softmax in base 2.
 //
 // Work split. One CTA per (sequence, KV head, 128 rows, split of the key
-// tiles). Warpgroups 0 and 1 are the softmax: two threads per row, each with
-// half of a key tile's scores (the row maximum is exchanged in shared memory,
-// the weight sums are joined at the end). Warpgroups 2 and 3 widen the packed
-// keys and values of the next tiles to binary16 operands in shared memory,
-// one key per thread, with the codes of two tiles ahead in registers. One
-// warp issues every tcgen05.mma: S = Q K^T and O += P V with P read from
-// tensor memory. S has two buffers, so one tile's softmax runs under the
-// products of its neighbours.
+// tiles), 25 warps with a role each:
+//  - 16 softmax warps: warp (w, q) takes a quarter w of a key tile's columns
+//    for the 32 rows of tensor-memory quarter q, as fragments (four rows per
+//    thread, a quarter of the columns each), so that a key's scale and offset
+//    are read once per four rows: with one row per thread those broadcast
+//    reads alone (128 x 128 x 8 bytes into registers) took 1024 cycles of a
+//    tile. The four warps of a quarter agree on the rare moves of a row's
+//    reference maximum by a barrier with a vote. Four warps per scheduler hide
+//    one another's latencies (two: 3800 cycles per tile and 128 rows).
+//  - 4 + 4 warps widen the packed keys and values of the next tiles to
+//    binary16 operands in shared memory, one key per thread, with the codes of
+//    two tiles ahead in registers.
+//  - 1 warp issues every tcgen05.mma: S = Q K^T, and O += P V with P read from
+//    tensor memory. S has two buffers, so one tile's softmax runs under the
+//    products of its neighbours.
 //
-// Precision. Key codes enter as c - 8, exact in binary16; the row's s and m
-// are applied in binary32 after the product. The rotated query is scaled by a
+// Precision. Key codes enter as 64 + c, exact in binary16 (the offset costs
+// the binary32 sum three of its bits); the row's s and m are applied in
+// binary32 after the product. The rotated query is scaled by a
 // power of two per row and split into binary16 hi + lo (about 22 bits): rounded to
 // one binary16 it would cost |z| 2^-12 in every exponent, which for outlier
 // keys (|z| of 10 and more) is several times the output's own rounding. p and
@@ -43,7 +51,7 @@ namespace kvq {
 
 namespace {
 
-constexpr int kPfThreads = 640;   // softmax 2 x 128, keys, values, and the issuing warp's group
+constexpr int kPfThreads = 896;   // softmax 512, keys 128, values 128, the issuing warp's group
 constexpr int kPfRows = 128;      // rows of a CTA
 constexpr uint32_t kPfTmemCols = 512;
 // A row's reference maximum moves only when a score exceeds it by more than
@@ -55,8 +63,8 @@ constexpr float kPfLift = 7.f;
 template <int D>
 struct PfCfg {
   static constexpr int KT = D == 128 ? 128 : 64;  // keys per tile
-  static constexpr int KC = KT / 2;               // keys per softmax thread
-  static constexpr int HC = D / 2;                // channels per softmax thread
+  static constexpr int KC = KT / 4;               // keys of a tile per softmax warp
+  static constexpr int HC = D / 4;                // channels of a row per softmax thread
   static constexpr int GRP = D * 16;              // bytes of 8 rows (D / 8 core matrices)
   // The query operand: in tensor memory at d = 128 (hi, then lo); in shared
   // memory at d = 256, where O leaves no columns for it. A product with A in
@@ -68,10 +76,17 @@ struct PfCfg {
   static constexpr int K_OFF = QT ? 0 : 2 * Q_B;
   static constexpr int K_B = KT * D * 2;
   static constexpr int V_OFF = K_OFF + NS * K_B;
-  static constexpr int PAR_OFF = V_OFF + NS * K_B;      // 4 slots x (scale, offset) x KT floats
+  // 4 slots of (scale, scale, offset, offset) per pair of keys
+  static constexpr int PAR_OFF = V_OFF + NS * K_B;
   static constexpr int BAD_OFF = PAR_OFF + 8 * KT * 4;  // 4 slots x 4 words
-  static constexpr int EX_OFF = BAD_OFF + 64;           // exchange: 2 slots x 2 halves x 128 floats
-  static constexpr int BAR_OFF = EX_OFF + 2 * 2 * kPfRows * 4;
+  static constexpr int EX_OFF = BAD_OFF + 64;           // exchange: 2 slots x 4 quarters x 128 floats
+  static constexpr int ROW_OFF = EX_OFF + 2 * 4 * kPfRows * 4;  // PfRowState of 128 rows
+  // rows of the query (d = 128) as copied in, and of the output on its way
+  // out; 272-byte pitch: eight threads on the same channels of consecutive
+  // rows meet different banks
+  static constexpr int QS_PITCH = 2 * D + 16;
+  static constexpr int QS_OFF = ROW_OFF + 32 * kPfRows;
+  static constexpr int BAR_OFF = QS_OFF + (QT ? kPfRows * QS_PITCH : 0);
   static constexpr int SMEM = BAR_OFF + 256;
   // tensor-memory columns: S0, S1, O, then Q (d = 128) or P (d = 256)
   static constexpr int O_COL = 2 * KT;
@@ -90,16 +105,14 @@ struct PfCfg {
 struct PfShared {
   uint64_t kf[2], ke[2];  // key stage filled / consumed
   uint64_t vf[2], ve[2];  // value stage filled / consumed
-  // parameters of tile j (slot j & 3: the keys run up to three tiles ahead of
-  // the softmax that reads them)
-  uint64_t mf[4];
-  uint64_t sf[2];   // S of tile j (buffer j & 1)
+  uint64_t sf[2];   // S of tile j (buffer j & 1), and the parameters of its keys
   uint64_t pf[2];   // P of tile j
-  uint64_t pv;      // O holds tile j's product
+  uint64_t pv[4];   // O holds tile j's product (slot j & 3)
   uint64_t qf;      // query operands staged
   uint32_t tmem;
-  int32_t lo, hi;            // positions some row of the CTA sees
-  int32_t all_lo, all_hi;    // positions every row sees
+  int32_t lo[4], hi[4];          // positions some row sees, per 32 rows
+  int32_t all_lo[4], all_hi[4];  // positions every row sees
+  int32_t dead;                  // a wait ran out
 };
 static_assert(sizeof(PfShared) <= 256, "shared state");
 
@@ -133,135 +146,151 @@ struct PrefillArgs {
   int32_t* err;
 };
 
+// Bounded wait. One that runs out (never expected) is the last of its CTA:
+// `dead` makes every later one return at once, so that all barriers still see
+// their arrivals and the CTA ends; the flag tells the caller to discard the
+// launch's outputs.
+__device__ __forceinline__ void pf_wait(uint32_t bar, uint32_t parity, volatile int32_t* dead) {
+  for (uint32_t it = 0; it < kMbarSpinLimit; ++it) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (__all_sync(0xffffffffu, done)) return;
+    if ((it & 1023u) == 1023u && *dead) return;
+  }
+  *dead = 1;
+}
+
 // Channels are visited in the order 0 4 1 5 2 6 3 7 inside each group of 8
 // (the nibble pairs that one mask extracts) by every operand.
 __device__ __forceinline__ constexpr int pf_perm(int i) { return (i >> 1) + 4 * (i & 1); }
 
-// Barrier of the two warps that share 32 rows (named barrier 1 + quarter),
+// Barrier of the four warps that share 32 rows (named barrier 1 + quarter),
 // with the ordering of their tensor-memory accesses.
-__device__ __forceinline__ void pf_pair_sync(int quarter) {
+__device__ __forceinline__ void pf_quarter_sync(int quarter) {
   tc_fence_before();
-  asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
+  asm volatile("bar.sync %0, 128;" ::"r"(1 + quarter) : "memory");
   tc_fence_after();
 }
-
-// One butterfly stage between columns [a, a + 32 n) and [b, b + 32 n).
-__device__ __forceinline__ void pf_cross(uint32_t scr, int a, int b, int n) {
-#pragma unroll 1
-  for (int c = 0; c < n; ++c) {
-    uint32_t x[32], y[32];
-    tmem_ld32(scr + a + 32 * c, x);
-    tmem_ld32(scr + b + 32 * c, y);
-    tmem_ld_wait();
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float p = __uint_as_float(x[i]), q = __uint_as_float(y[i]);
-      x[i] = __float_as_uint(p + q);
-      y[i] = __float_as_uint(p - q);
-    }
-    tmem_st32(scr + a + 32 * c, x);
-    tmem_st32(scr + b + 32 * c, y);
-  }
-  tmem_st_wait();
+// The same barrier with a vote: whether `p` holds in any of its 128 threads.
+__device__ __forceinline__ bool pf_quarter_any(int quarter, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "bar.red.or.pred p, %2, 128, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)p), "r"(1 + quarter)
+      : "memory");
+  return r != 0;
 }
 
-// The rotation (or its inverse with INV) of a row held as D binary32 columns
-// of its tensor-memory lane at `scr`, by the row's two threads (w = 0, 1 own
-// channels [w D/2, (w + 1) D/2)); warp-collective for both. Stages inside 64
-// channels run in registers, wider ones between tensor-memory columns.
-template <int D, bool INV>
-__device__ __forceinline__ void pf_rotate(uint32_t scr, int w, int quarter, int rot_kind, int lgb,
-                                          const float* tbl) {
+// One butterfly stage between columns [a, a + 16) and [b, b + 16) of a row.
+__device__ __forceinline__ void pf_cross16(uint32_t scr, int a, int b) {
+  uint32_t x[16], y[16];
+  tmem_ld16(scr + a, x);
+  tmem_ld16(scr + b, y);
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float p = __uint_as_float(x[i]), q = __uint_as_float(y[i]);
+    x[i] = __float_as_uint(p + q);
+    y[i] = __float_as_uint(p - q);
+  }
+  tmem_st16(scr + a, x);
+  tmem_st16(scr + b, y);
+}
+
+// The rotation of 32 channels [ch, ch + 32) as far as it stays inside them:
+// sign flips, butterflies below 32 and the scale, or the quaternion blocks.
+template <bool INV>
+__device__ __noinline__ void pf_rotate_quat(float (&x)[32], int ch, int rot_kind, const float* tbl) {
+  if (rot_kind == KVQ_ROT_QUAT) {
+    if (INV) quat_inv_regs<32>(x, tbl, ch); else quat_regs<32>(x, tbl, ch);
+  } else if (rot_kind == KVQ_ROT_QUAT_FAST) {
+    if (INV) quat_fast_inv_regs<32>(x, tbl, ch); else quat_fast_regs<32>(x, tbl, ch);
+  } else {
+    quat_mat_fly_regs<32, INV>(x, tbl, ch);
+  }
+}
+template <bool INV>
+__device__ __forceinline__ void pf_rotate_in(float (&x)[32], int ch, int rot_kind, int lgb,
+                                             const float* tbl) {
   if (rot_kind == KVQ_ROT_NONE) return;
-  const int c0 = w * (D / 2);
   if (rot_kind == KVQ_ROT_HADAMARD || rot_kind == KVQ_ROT_HADAMARD_SIGNED) {
     const bool sgn = rot_kind == KVQ_ROT_HADAMARD_SIGNED;
     const float cb = hadamard_scale(lgb);
-#pragma unroll 1
-    for (int h = 0; h < D / 128; ++h) {
-      const int ch = c0 + 64 * h;
-      uint32_t r[2][32];
-      tmem_ld32(scr + ch, r[0]);
-      tmem_ld32(scr + ch + 32, r[1]);
-      tmem_ld_wait();
-      float x[64];
+    if (!INV && sgn) {
 #pragma unroll
-      for (int i = 0; i < 64; ++i) x[i] = __uint_as_float(r[i >> 5][i & 31]);
-      if (!INV && sgn) {
-#pragma unroll
-        for (int i = 0; i < 64; ++i) x[i] *= __ldg(tbl + ch + i);
-      }
-      fwht_regs<64, 4>(x);
-#pragma unroll
-      for (int st = 16; st < 64; st <<= 1) {
-        if ((1 << lgb) <= st) break;
-#pragma unroll
-        for (int i = 0; i < 64; i += 2)
-          if ((i & st) == 0) {
-            const uint64_t a = pk(x[i], x[i + 1]), b = pk(x[i + st], x[i + st + 1]);
-            const float2 s = upk(add2(a, b)), d = upk(sub2(a, b));
-            x[i] = s.x; x[i + 1] = s.y; x[i + st] = d.x; x[i + st + 1] = d.y;
-          }
-      }
-#pragma unroll
-      for (int i = 0; i < 64; ++i) r[i >> 5][i & 31] = __float_as_uint(x[i] * cb);
-      tmem_st32(scr + ch, r[0]);
-      tmem_st32(scr + ch + 32, r[1]);
+      for (int i = 0; i < 32; ++i) x[i] *= __ldg(tbl + ch + i);
     }
-    tmem_st_wait();
-    if (lgb >= 7) {
-      if (D == 128) {  // both threads' halves: 32 column pairs each
-        pf_pair_sync(quarter);
-        pf_cross(scr, 32 * w, 64 + 32 * w, 1);
-        pf_pair_sync(quarter);
-      } else {
-        pf_cross(scr, c0, c0 + 64, 2);
-      }
-    }
-    if (D == 256 && lgb == 8) {
-      pf_pair_sync(quarter);
-      pf_cross(scr, 64 * w, 128 + 64 * w, 2);
-      pf_pair_sync(quarter);
-    }
-    if (INV && sgn) {
-#pragma unroll 1
-      for (int c = 0; c < D / 64; ++c) {
-        uint32_t r[32];
-        tmem_ld32(scr + c0 + 32 * c, r);
-        tmem_ld_wait();
+    if (lgb > 4) fwht_regs<32, 5>(x); else fwht_regs<32, 4>(x);
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          r[i] = __float_as_uint(__uint_as_float(r[i]) * __ldg(tbl + c0 + 32 * c + i));
-        tmem_st32(scr + c0 + 32 * c, r);
-      }
-      tmem_st_wait();
-    }
+    for (int i = 0; i < 32; ++i) x[i] *= cb;
     return;
   }
+  pf_rotate_quat<INV>(x, ch, rot_kind, tbl);
+}
+// The wider Hadamard stages of a row in D tensor-memory columns at `scr`, by
+// the row's four threads (w = 0..3); each stage's column pairs are dealt out
+// evenly. Every thread has stored its own channels before.
+template <int D>
+__device__ __forceinline__ void pf_rotate_out(uint32_t scr, int w, int quarter, int rot_kind, int lgb) {
+  if (rot_kind != KVQ_ROT_HADAMARD && rot_kind != KVQ_ROT_HADAMARD_SIGNED) return;
 #pragma unroll 1
-  for (int c = 0; c < D / 64; ++c) {
-    uint32_t r[32];
-    tmem_ld32(scr + c0 + 32 * c, r);
-    tmem_ld_wait();
-    float x[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
-    if (rot_kind == KVQ_ROT_QUAT) {
-      if (INV) quat_inv_regs<32>(x, tbl, c0 + 32 * c); else quat_regs<32>(x, tbl, c0 + 32 * c);
-    } else if (rot_kind == KVQ_ROT_QUAT_FAST) {
-      if (INV) quat_fast_inv_regs<32>(x, tbl, c0 + 32 * c);
-      else quat_fast_regs<32>(x, tbl, c0 + 32 * c);
-    } else {
-      quat_mat_fly_regs<32, INV>(x, tbl, c0 + 32 * c);
+  for (int lg = 5; lg < lgb; ++lg) {
+    tmem_st_wait();
+    pf_quarter_sync(quarter);
+    // the D / 2 column pairs of distance 2^lg, 16 at a time: pair group k
+    // starts at column (k / g) 2^(lg + 1) + 16 (k % g), g = 2^lg / 16
+#pragma unroll 1
+    for (int k = w; k < D / 32; k += 4) {
+      const int g = (1 << lg) >> 4;
+      const int a = (k / g) * (2 << lg) + 16 * (k % g);
+      pf_cross16(scr, a, a + (1 << lg));
     }
-#pragma unroll
-    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(x[i]);
-    tmem_st32(scr + c0 + 32 * c, r);
   }
   tmem_st_wait();
+  pf_quarter_sync(quarter);
 }
 
-// Row state of one softmax thread.
+// The power of two that brings a row's largest |q^| into [2^12, 2^13) (lo
+// then keeps its bits above the binary16 subnormals) and its inverse; a zero
+// query scores 0.
+__device__ __forceinline__ void pf_query_scale(float amax, float& mul, float& rs) {
+  int e = 12 - (((__float_as_int(amax) >> 23) & 0xFF) - 127);
+  e = min(max(e, -126), 126);
+  mul = amax > 0.f ? __int_as_float((e + 127) << 23) : 0.f;
+  rs = amax > 0.f ? __int_as_float((127 - e) << 23) : 1.f;
+}
+
+// x0, x1 as binary16 hi + lo pairs; returns the sum of what they hold.
+__device__ __forceinline__ float pf_split(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  const __half2 hh = __floats2half2_rn(x0, x1);
+  const float2 f = __half22float2(hh);
+  const __half2 ll = __floats2half2_rn(x0 - f.x, x1 - f.y);
+  const float2 g = __half22float2(ll);
+  hi = h2_as_u32(hh);
+  lo = h2_as_u32(ll);
+  return (f.x + g.x) + (f.y + g.y);
+}
+
+// What the softmax keeps per row in shared memory.
+struct alignas(16) PfRowState {
+  int lo, hi, p;    // interval and position
+  float slope2;     // slope of the distance bias, base 2
+  float rs, qsum;   // 2^-e of the scaled query, and its sum
+  float M, pad;     // at the end: reference exponent M - lift
+};
+static_assert(sizeof(PfRowState) == 32, "row state");
+
+// The row of a softmax thread in the first and last part.
 struct PfRow {
   bool valid;     // the row exists
   int64_t row;    // token * Hq + head
@@ -270,11 +299,15 @@ struct PfRow {
 };
 
 // Four bytes of codes (8 channels) as binary16 pairs in the operands' channel
-// order: c - 8, exactly.
+// order: 64 + c, exactly (the nibble OR-ed into bits 4-7 of the binary16 value
+// 64, 0x5400; seven logic operations and no arithmetic).
 __device__ __forceinline__ uint4 pf_codes_k(uint32_t x) {
-  const uint32_t y = x >> 8;
-  return make_uint4(nib_c8(x, 0x000F000Fu, 0), nib_c8(x, 0x00F000F0u, 1),
-                    nib_c8(y, 0x000F000Fu, 0), nib_c8(y, 0x00F000F0u, 1));
+  auto at = [](uint32_t w) {
+    uint32_t t;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(t) : "r"(w), "r"(0x00F000F0u), "r"(0x54005400u));
+    return t;
+  };
+  return make_uint4(at(x << 4), at(x), at(x >> 4), at(x >> 8));
 }
 // The dequantized values c s + m of 8 channels, rounded once.
 __device__ __forceinline__ uint4 pf_codes_v(uint32_t x, __half2 s2, __half2 m2) {
@@ -292,6 +325,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
   constexpr int KT = C::KT, KC = C::KC, NS = C::NS;
   extern __shared__ __align__(1024) uint8_t smem[];
   PfShared& sh = *reinterpret_cast<PfShared*>(smem + C::BAR_OFF);
+  PfRowState* const rst = reinterpret_cast<PfRowState*>(smem + C::ROW_OFF);
   const int tid = threadIdx.x, warp = tid / kWarp, lane = tid % kWarp;
   const int wg = tid / 128;
 
@@ -336,41 +370,53 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
   if (tid == 0) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.kf[i], 128);
+      mbar_init(&sh.kf[i], 4);
       mbar_init(&sh.ke[i], 1);
-      mbar_init(&sh.vf[i], 128);
+      mbar_init(&sh.vf[i], 4);
       mbar_init(&sh.ve[i], 1);
-      mbar_init(&sh.sf[i], 1);
-      mbar_init(&sh.pf[i], 256);
+      mbar_init(&sh.sf[i], 2);
+      mbar_init(&sh.pf[i], 16);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) mbar_init(&sh.mf[i], 128);
-    mbar_init(&sh.pv, 1);
-    mbar_init(&sh.qf, 256);
-    sh.lo = INT_MAX;
-    sh.hi = 0;
-    sh.all_lo = 0;
-    sh.all_hi = INT_MAX;
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&sh.pv[i], 1);
+    }
+    mbar_init(&sh.qf, 16);
+    sh.dead = 0;
     mbar_fence_init();
   }
-  if (warp == 16) {
+  if (warp == 24) {
     tmem_alloc(&sh.tmem, kPfTmemCols);
     tmem_relinquish();
   }
-  __syncthreads();
+  // ---- the query rows' copies (d = 128: whole rows, coalesced, to shared memory)
+  if (C::QT && wg < 4) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = 32 * k + (tid >> 4);
+      const int ri = (int)r0 + r;
+      const bool ok = ri < rows;
+      const int i = ok ? ri / a.G : 0;
+      const int hd = ok ? h * a.G + ri - i * a.G : 0;
+      cp_async16_zf(smem + C::QS_OFF + r * C::QS_PITCH + 16 * (tid & 15),
+                    a.q + (int64_t)(ok ? q0 + i : 0) * a.q_stride + (int64_t)hd * D + 8 * (tid & 15),
+                    ok ? 16u : 0u);
+    }
+    cp_async_commit();
+  }
 
   // ---- each row's interval, and what the CTA sees
   PfRow R;
   R.valid = false;
   R.row = 0;
   R.tok = R.head = R.p = R.lo = R.hi = 0;
-  if (wg < 2) {
+  if (wg < 4) {
     const int64_t ri = r0 + (tid & 127);
     R.valid = ri < rows;
     if (R.valid) {
-      const int i = (int)(ri / a.G);
+      const int i = (int)ri / a.G;
       R.tok = q0 + i;
-      R.head = h * a.G + (int)(ri - (int64_t)i * a.G);
+      R.head = h * a.G + (int)ri - i * a.G;
       R.row = (int64_t)R.tok * a.Hq + R.head;
       bool ok = seq_ok;
       if (a.shared_len >= 0) {
@@ -379,7 +425,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
         ok = ok && Ls >= a.shared_len && Ls <= a.max_seq_len && Ls > 0 &&
              ((Ls + (1 << a.lgP) - 1) >> a.lgP) <= a.bt_stride &&
              (a.rope == nullptr || Ls <= a.rope_max_pos);
-        if (!ok && Ls != 0) raise_flag(a.err, KVQ_ERRF_LEN);
+        if (!ok && Ls != 0 && wg == 0) raise_flag(a.err, KVQ_ERRF_LEN);
         R.p = Ls - 1;
       } else {
         R.p = L - n + i;
@@ -390,21 +436,31 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
       if (a.window > 0 && R.p >= a.window) R.lo = R.p - a.window + 1;
       if (a.first_pos != nullptr) R.lo = max(R.lo, a.first_pos[R.tok]);
       if (!ok || R.lo >= R.hi) R.lo = R.hi = 0;
-      if (wg == 0) {
-        if (R.hi > 0) {
-          atomicMin(&sh.lo, R.lo);
-          atomicMax(&sh.hi, R.hi);
-        }
-        atomicMax(&sh.all_lo, R.lo);
-        atomicMin(&sh.all_hi, R.hi);
+    }
+    if (wg == 0) {
+      const int lo = __reduce_min_sync(0xffffffffu, R.hi > 0 ? R.lo : INT_MAX);
+      const int hi = __reduce_max_sync(0xffffffffu, R.hi);
+      const int alo = __reduce_max_sync(0xffffffffu, R.valid ? R.lo : 0);
+      const int ahi = __reduce_min_sync(0xffffffffu, R.valid ? R.hi : INT_MAX);
+      if (lane == 0) {
+        sh.lo[warp] = lo;
+        sh.hi[warp] = hi;
+        sh.all_lo[warp] = alo;
+        sh.all_hi[warp] = ahi;
       }
+      PfRowState& w = rst[tid];
+      w.lo = R.lo;
+      w.hi = R.hi;
+      w.p = R.p;
+      w.slope2 = OPT && a.alibi != nullptr && R.valid ? a.alibi[R.head] * 1.4426950408889634f : 0.f;
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  const int kv_lo = sh.lo, kv_hi = sh.hi;
+  const int kv_lo = min(min(sh.lo[0], sh.lo[1]), min(sh.lo[2], sh.lo[3]));
+  const int kv_hi = max(max(sh.hi[0], sh.hi[1]), max(sh.hi[2], sh.hi[3]));
   int t0 = 0, t1 = 0;  // key tiles of this split
   if (kv_hi > kv_lo) {
     const int ta = kv_lo / KT, tb = (kv_hi + KT - 1) / KT;
@@ -413,36 +469,47 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
   }
   const int ntile = t1 - t0;
 
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (!mbar_wait(bar, parity)) {
-      raise_flag(a.err, KVQ_ERRF_TIMEOUT);
-      return false;
-    }
-    return true;
+  const uint32_t bars = smem_u32(&sh);
+  auto wait = [&](const uint64_t* bar, uint32_t parity) {
+    pf_wait(bars + (uint32_t)(reinterpret_cast<const uint8_t*>(bar) -
+                              reinterpret_cast<const uint8_t*>(&sh)), parity, &sh.dead);
   };
 
-  if (wg < 2) {
-    // =========================== softmax: two threads per row
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+  // One arrival per warp, after all its lanes: a barrier takes the arrivals of
+  // a warp's 32 lanes one after the other (with an arrival per thread, 512 per
+  // tile, a tile took twice its time).
+  auto arrive = [&](uint64_t* bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
+
+  if (wg < 4) {
+    // =========================== softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
     const int qd = warp & 3;                    // lane quarter of the warp
     const int row = tid & 127;
     const uint32_t lane_base = (uint32_t)(qd * 32) << 16;
     const uint32_t o_col = tmem + lane_base + C::O_COL;
+    const int c0 = wg * C::HC;                  // the thread's channels of its row
     float* const ex = reinterpret_cast<float*>(smem + C::EX_OFF);
-    float rs = 1.f, qsum = 0.f;  // 2^-e of the row's scaled query, and its sum
+    if (C::QT) {  // every query row is in shared memory
+      cp_async_wait<0>();
+      asm volatile("bar.sync 7, 512;" ::: "memory");
+    }
     if (ntile > 0) {
       // ---- the query row: RoPE, rotation (O's columns as scratch), then hi + lo
-      const int c0 = wg * C::HC;
-      const __half* src = a.q + (int64_t)R.tok * a.q_stride + (int64_t)R.head * D + c0;
       const float* cs =
           a.rope != nullptr && R.valid && R.hi > 0 ? a.rope + (int64_t)R.p * D + c0 : nullptr;
+      const uint4* src =
+          C::QT ? reinterpret_cast<const uint4*>(smem + C::QS_OFF + row * C::QS_PITCH + 2 * c0)
+                : reinterpret_cast<const uint4*>(a.q + (int64_t)R.tok * a.q_stride +
+                                                 (int64_t)R.head * D + c0);
 #pragma unroll 1
-      for (int c = 0; c < C::HC / 32; ++c) {
+      for (int c = 0; c < C::HC; c += 32) {
         float x[32];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint4 u = R.valid ? __ldg(reinterpret_cast<const uint4*>(src + 32 * c) + k)
-                                  : make_uint4(0u, 0u, 0u, 0u);
+          const uint4 u = C::QT || R.valid ? src[c / 8 + k] : make_uint4(0u, 0u, 0u, 0u);
           const uint32_t w4[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -451,236 +518,284 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
             x[8 * k + 2 * e + 1] = f.y;
           }
         }
-        if (cs != nullptr) rope_regs<32>(x, cs + 32 * c);
+        if (cs != nullptr) rope_regs<32>(x, cs + c);
         __syncwarp();
+        pf_rotate_in<false>(x, c0 + c, a.rot_kind, a.lgb, a.quat);
         uint32_t r[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(x[i]);
-        tmem_st32(o_col + c0 + 32 * c, r);
+        tmem_st32(o_col + c0 + c, r);
       }
       tmem_st_wait();
-      pf_rotate<D, false>(o_col, wg, qd, a.rot_kind, a.lgb, a.quat);
+      pf_rotate_out<D>(o_col, wg, qd, a.rot_kind, a.lgb);
       float amax = 0.f;
 #pragma unroll 1
-      for (int c = 0; c < C::HC / 32; ++c) {
+      for (int c = 0; c < C::HC; c += 32) {
         uint32_t r[32];
-        tmem_ld32(o_col + c0 + 32 * c, r);
+        tmem_ld32(o_col + c0 + c, r);
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf(__uint_as_float(r[i])));
       }
       ex[wg * kPfRows + row] = amax;
-      pf_pair_sync(qd);
-      amax = fmaxf(amax, ex[(wg ^ 1) * kPfRows + row]);
-      // the power of two that brings the largest |q^| into [2^12, 2^13): lo
-      // keeps its bits above the binary16 subnormals
-      int e = 12 - (((__float_as_int(amax) >> 23) & 0xFF) - 127);
-      e = min(max(e, -126), 126);
-      const float mul = amax > 0.f ? __int_as_float((e + 127) << 23) : 0.f;
-      rs = amax > 0.f ? __int_as_float((127 - e) << 23) : 1.f;  // (a zero query scores 0)
-      uint8_t* const qh = smem + (row >> 3) * C::GRP + (row & 7) * 16;
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + qd) : "memory");
+      amax = fmaxf(fmaxf(ex[row], ex[kPfRows + row]),
+                   fmaxf(ex[2 * kPfRows + row], ex[3 * kPfRows + row]));
+      float mul, rs, qsum = 0.f;
+      pf_query_scale(amax, mul, rs);
 #pragma unroll 1
-      for (int c = 0; c < C::HC / 32; ++c) {
+      for (int c = 0; c < C::HC; c += 32) {
         uint32_t r[32], hw[16], lw[16];
-        tmem_ld32(o_col + c0 + 32 * c, r);
+        tmem_ld32(o_col + c0 + c, r);
         tmem_ld_wait();
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
           const int i = 8 * (k >> 2) + (k & 3);
-          const float x0 = __uint_as_float(r[i]) * mul, x1 = __uint_as_float(r[i + 4]) * mul;
-          const __half2 hh = __floats2half2_rn(x0, x1);
-          const float2 f = __half22float2(hh);
-          const __half2 ll = __floats2half2_rn(x0 - f.x, x1 - f.y);
-          const float2 g = __half22float2(ll);
-          qsum += (f.x + g.x) + (f.y + g.y);
-          hw[k] = h2_as_u32(hh);
-          lw[k] = h2_as_u32(ll);
+          qsum += pf_split(__uint_as_float(r[i]) * mul, __uint_as_float(r[i + 4]) * mul, hw[k], lw[k]);
         }
         if (C::QT) {
-          const uint32_t qc = tmem + lane_base + C::Q_COL + (c0 + 32 * c) / 2;
+          const uint32_t qc = tmem + lane_base + C::Q_COL + (c0 + c) / 2;
           tmem_st16(qc, hw);
           tmem_st16(qc + D / 2, lw);
         } else {
+          uint8_t* const qh = smem + (row >> 3) * C::GRP + (row & 7) * 16 + ((c0 + c) >> 3) * 128;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            uint8_t* dst = qh + ((c0 >> 3) + 4 * c + k) * 128;
-            *reinterpret_cast<uint4*>(dst) =
+            *reinterpret_cast<uint4*>(qh + 128 * k) =
                 make_uint4(hw[4 * k], hw[4 * k + 1], hw[4 * k + 2], hw[4 * k + 3]);
-            *reinterpret_cast<uint4*>(dst + C::Q_B) =
+            *reinterpret_cast<uint4*>(qh + 128 * k + C::Q_B) =
                 make_uint4(lw[4 * k], lw[4 * k + 1], lw[4 * k + 2], lw[4 * k + 3]);
           }
         }
       }
       if (C::QT) tmem_st_wait(); else fence_async_smem();
       tc_fence_before();
-      mbar_arrive(&sh.qf);
-      ex[2 * kPfRows + wg * kPfRows + row] = qsum;
-      pf_pair_sync(qd);
-      qsum += ex[2 * kPfRows + (wg ^ 1) * kPfRows + row];
-      pf_pair_sync(qd);
+      arrive(&sh.qf);
+      ex[(4 + wg) * kPfRows + row] = qsum;
+      pf_quarter_sync(qd);
+      if (wg == 0) {
+        rst[row].rs = rs;
+        rst[row].qsum = (qsum + ex[5 * kPfRows + row]) + (ex[6 * kPfRows + row] + ex[7 * kPfRows + row]);
+      }
+      pf_quarter_sync(qd);
     }
 
-    float M = -INFINITY, l = 0.f;
-    const float slope2 = OPT && a.alibi != nullptr && R.valid
-                             ? __ldg(a.alibi + R.head) * 1.4426950408889634f : 0.f;
-    const int all_lo = sh.all_lo, all_hi = sh.all_hi;
-    const int k0 = wg * KC;  // the thread's keys of a tile: [k0, k0 + KC)
-    bool live = true;
+    // ---- four rows per thread: row rr at 32 qd + 8 rr + lane / 4,
+    // columns 8 i + 2 (lane % 4) + {0, 1} of the warp's KC keys
+    constexpr int NI = KC / 8;  // column groups
+    const int jl = lane & 3;
+    const int row0 = 32 * qd + (lane >> 2);
+    const int all_lo = sh.all_lo[qd], all_hi = sh.all_hi[qd];
+    const int k0 = wg * KC;  // the warp's keys of a tile: [k0, k0 + KC)
+    // per row: the reference maximum M, kept as M + slack and as the exponent's
+    // offset (lift - M; 0 before any score)
+    float thr[4], off[4], l[4], rs[4], qs[4];
+#pragma unroll
+    for (int rr = 0; rr < 4; ++rr) {
+      thr[rr] = -INFINITY;
+      off[rr] = 0.f;
+      l[rr] = 0.f;
+      rs[rr] = rst[row0 + 8 * rr].rs;
+      qs[rr] = rst[row0 + 8 * rr].qsum;
+    }
     for (int j = 0; j < ntile; ++j) {
       const uint32_t s_col = tmem + lane_base + (j & 1) * KT + k0;
-      live = wait(&sh.mf[j & 3], (j >> 2) & 1) && wait(&sh.sf[j & 1], (j >> 1) & 1);
-      live = __all_sync(0xffffffffu, live);
-      if (!live) break;
+      wait(&sh.sf[j & 1], (j >> 1) & 1);
       tc_fence_after();
-      uint32_t zr[KC / 32][32];
+      // zr[rb][4 i + e]: row rr = 2 rb + e / 2, column 8 i + 2 jl + e % 2
+      uint32_t zr[2][4 * NI];
 #pragma unroll
-      for (int c = 0; c < KC / 32; ++c) tmem_ld32(s_col + 32 * c, zr[c]);
-      tmem_ld_wait();
-      const float* ks = reinterpret_cast<const float*>(smem + C::PAR_OFF) + (j & 3) * 2 * KT + k0;
+      for (int rb = 0; rb < 2; ++rb) tmem_ld_frag<4 * NI>(s_col + ((uint32_t)(16 * rb) << 16), zr[rb]);
+      const float4* ks = reinterpret_cast<const float4*>(smem + C::PAR_OFF) + (j & 3) * (KT / 2) +
+                         k0 / 2 + jl;
+      const uint32_t bad = *reinterpret_cast<const uint32_t*>(smem + C::BAD_OFF + (j & 3) * 16 +
+                                                              4 * (k0 / 32));
       const int base = (t0 + j) * KT + k0;
+      tmem_ld_wait();
       // z / rs = s'_j dot + m'_j qsum
-      const uint64_t qs2 = pk(qsum, qsum);
 #pragma unroll
-      for (int c = 0; c < KC / 4; ++c) {
-        const float4 sv = *reinterpret_cast<const float4*>(ks + 4 * c);
-        const float4 mv = *reinterpret_cast<const float4*>(ks + KT + 4 * c);
-        uint32_t* z = &zr[c >> 3][(4 * c) & 31];
-        const float2 a0 = upk(fma2(pk(__uint_as_float(z[0]), __uint_as_float(z[1])),
-                                   pk(sv.x, sv.y), mul2(pk(mv.x, mv.y), qs2)));
-        const float2 a1 = upk(fma2(pk(__uint_as_float(z[2]), __uint_as_float(z[3])),
-                                   pk(sv.z, sv.w), mul2(pk(mv.z, mv.w), qs2)));
-        z[0] = __float_as_uint(a0.x);
-        z[1] = __float_as_uint(a0.y);
-        z[2] = __float_as_uint(a1.x);
-        z[3] = __float_as_uint(a1.y);
-      }
-      float mul = rs;  // what is left to multiply z by
-      if (OPT) {
-        mul = 1.f;
-        if (a.capk > 0.f) {
-          // cap tanh(z / cap) = cap (1 - 2 / (1 + e^(2 z / cap)))
-          const float k = rs * a.capk;
+      for (int i = 0; i < NI; ++i) {
+        const float4 pv = ks[4 * i];
 #pragma unroll
-          for (int c = 0; c < KC; ++c) {
-            const float e = fast_exp2(__uint_as_float(zr[c >> 5][c & 31]) * k);
-            zr[c >> 5][c & 31] =
-                __float_as_uint(fmaf(fast_rcp(1.f + e), -2.f * a.cap2, a.cap2));
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < KC; ++c)
-            zr[c >> 5][c & 31] = __float_as_uint(__uint_as_float(zr[c >> 5][c & 31]) * rs);
+        for (int rr = 0; rr < 4; ++rr) {
+          uint32_t* z = &zr[rr >> 1][4 * i + 2 * (rr & 1)];
+          const float2 f = upk(fma2(pk(__uint_as_float(z[0]), __uint_as_float(z[1])), pk(pv.x, pv.y),
+                                    mul2(pk(pv.z, pv.w), pk(qs[rr], qs[rr]))));
+          z[0] = __float_as_uint(f.x);
+          z[1] = __float_as_uint(f.y);
         }
-        if (a.alibi != nullptr) {
-          const float d0 = (float)(base - R.p);
+      }
+      if (OPT) {
 #pragma unroll
-          for (int c = 0; c < KC; ++c)
-            zr[c >> 5][c & 31] = __float_as_uint(
-                fmaf(-slope2, fabsf(d0 + (float)c), __uint_as_float(zr[c >> 5][c & 31])));
+        for (int rr = 0; rr < 4; ++rr) {
+          uint32_t* const z = &zr[rr >> 1][2 * (rr & 1)];  // elements 4 i + e
+          if (a.capk > 0.f) {
+            // cap tanh(z / cap) = cap (1 - 2 / (1 + e^(2 z / cap)))
+            const float k = rs[rr] * a.capk;
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                z[4 * i + e] = __float_as_uint(
+                    fmaf(fast_rcp(1.f + fast_exp2(__uint_as_float(z[4 * i + e]) * k)),
+                         -2.f * a.cap2, a.cap2));
+          } else {
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                z[4 * i + e] = __float_as_uint(__uint_as_float(z[4 * i + e]) * rs[rr]);
+          }
+          if (a.alibi != nullptr) {
+            const PfRowState& w = rst[row0 + 8 * rr];
+            const float sl = w.slope2, d0 = (float)(base + 2 * jl - w.p);
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                z[4 * i + e] = __float_as_uint(
+                    fmaf(-sl, fabsf(d0 + (float)(8 * i + e)), __uint_as_float(z[4 * i + e])));
+          }
         }
       }
       // positions outside the row's interval, and keys of a bad page
-      const uint4 bad = *reinterpret_cast<const uint4*>(smem + C::BAD_OFF + (j & 3) * 16);
-      const bool anybad = (bad.x | bad.y | bad.z | bad.w) != 0u;
-      if (anybad || base < all_lo || base + KC > all_hi) {
-        const int lo = R.lo - base, hi = R.hi - base;
-        // bad-page words of the thread's keys
-        const uint32_t bw[2] = {KC == 64 ? (wg ? bad.z : bad.x) : (wg ? bad.y : bad.x),
-                                KC == 64 ? (wg ? bad.w : bad.y) : 0u};
+      if (base < all_lo || base + KC > all_hi) {
 #pragma unroll
-        for (int w = 0; w < KC / 32; ++w) {
-          // bits [lo, hi) of this 32-key word, less the bad ones
-          const int l0 = min(max(lo - 32 * w, 0), 32), h0 = min(max(hi - 32 * w, 0), 32);
-          uint32_t m = h0 >= 32 ? 0xffffffffu : (1u << h0) - 1u;
-          m &= l0 >= 32 ? 0u : 0xffffffffu << l0;
-          m &= ~bw[w];
+        for (int rr = 0; rr < 4; ++rr) {
+          uint32_t* const z = &zr[rr >> 1][2 * (rr & 1)];
+          const PfRowState& w = rst[row0 + 8 * rr];
+          const int lo = w.lo - base - 2 * jl;
+          const uint32_t len = (uint32_t)(w.hi - w.lo);
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (!((m >> i) & 1u)) zr[w][i] = 0xff800000u;
+          for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if ((uint32_t)(8 * i + e - lo) >= len) z[4 * i + e] = 0xff800000u;
         }
       }
-      float mx0 = -INFINITY, mx1 = -INFINITY;
+      if (bad != 0u) {
+        const uint32_t bw = bad >> (k0 & 31);
 #pragma unroll
-      for (int c = 0; c < KC; c += 4) {
-        const uint32_t* z = &zr[c >> 5][c & 31];
-        mx0 = max3(mx0, __uint_as_float(z[0]), __uint_as_float(z[1]));
-        mx1 = max3(mx1, __uint_as_float(z[2]), __uint_as_float(z[3]));
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if ((bw >> (8 * i + 2 * jl + e)) & 1u) {
+              zr[0][4 * i + e] = zr[0][4 * i + 2 + e] = 0xff800000u;
+              zr[1][4 * i + e] = zr[1][4 * i + 2 + e] = 0xff800000u;
+            }
       }
-      float mx = fmaxf(mx0, mx1) * mul;
-      float* const exj = ex + (j & 1) * 2 * kPfRows;
-      exj[wg * kPfRows + row] = mx;
-      asm volatile("bar.sync %0, 64;" ::"r"(1 + qd) : "memory");
-      mx = fmaxf(mx, exj[(wg ^ 1) * kPfRows + row]);
-      const bool move = mx > M + kPfSlack;
-      // every phase of pv is waited for once, before the arrival that lets the
-      // next one complete (a parity names one of two phases only)
-      bool waited = j == 0;
-      if (__any_sync(0xffffffffu, move)) {
-        const float Mn = move ? mx : M;
-        const float alpha = !move ? 1.f : M == -INFINITY ? 0.f : fast_exp2(M - Mn);
-        M = Mn;
-        l *= alpha;
+      // row maxima: of the thread's columns, then of the row's four lanes
+      float mx[4];
+#pragma unroll
+      for (int rr = 0; rr < 4; ++rr) {
+        const uint32_t* const z = &zr[rr >> 1][2 * (rr & 1)];
+        float m0 = fmaxf(__uint_as_float(z[0]), __uint_as_float(z[1]));
+#pragma unroll
+        for (int i = 1; i < NI; ++i)
+          m0 = max3(m0, __uint_as_float(z[4 * i]), __uint_as_float(z[4 * i + 1]));
+        mx[rr] = OPT ? m0 : m0 * rs[rr];
+      }
+      bool move = false;
+#pragma unroll
+      for (int rr = 0; rr < 4; ++rr) move = move || mx[rr] > thr[rr];
+      // a score of the quarter's rows exceeds its reference: all four warps
+      // take the rows' maxima over the whole tile
+      if (pf_quarter_any(qd, move)) {
+        float* const exj = ex + (j & 1) * 4 * kPfRows;
+#pragma unroll
+        for (int rr = 0; rr < 4; ++rr) {
+          mx[rr] = fmaxf(mx[rr], __shfl_xor_sync(0xffffffffu, mx[rr], 1));
+          mx[rr] = fmaxf(mx[rr], __shfl_xor_sync(0xffffffffu, mx[rr], 2));
+          if (jl == 0) exj[wg * kPfRows + row0 + 8 * rr] = mx[rr];
+        }
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + qd) : "memory");
+        float al[4];
+#pragma unroll
+        for (int rr = 0; rr < 4; ++rr) {
+          const float* const e = exj + row0 + 8 * rr;
+          mx[rr] = fmaxf(fmaxf(e[0], e[kPfRows]), fmaxf(e[2 * kPfRows], e[3 * kPfRows]));
+          const bool mv = mx[rr] > thr[rr];
+          const float no = mv ? kPfLift - mx[rr] : off[rr];
+          al[rr] = thr[rr] == -INFINITY ? 0.f : fast_exp2(no - off[rr]);
+          off[rr] = no;
+          if (mv) thr[rr] = mx[rr] + kPfSlack;
+          l[rr] *= al[rr];
+        }
         if (j > 0) {
-          waited = true;
-          live = __all_sync(0xffffffffu, wait(&sh.pv, (j - 1) & 1));
-          if (!live) break;
+          // (S of tile j implies the product of tile j - 2: the parity is not ambiguous)
+          wait(&sh.pv[(j - 1) & 3], ((j - 1) >> 2) & 1);
           tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < C::HC / 16; ++c) {
-            uint32_t o[16];
-            tmem_ld16(o_col + wg * C::HC + 16 * c, o);
-            tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-            tmem_st16(o_col + wg * C::HC + 16 * c, o);
-          }
+          for (int rb = 0; rb < 2; ++rb)
+#pragma unroll 1
+            for (int c = 0; c < C::HC; c += 32) {
+              const uint32_t at = o_col + ((uint32_t)(16 * rb) << 16) + c0 + c;
+              uint32_t o[16];
+              tmem_ld_frag<16>(at, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                o[i] = __float_as_uint(__uint_as_float(o[i]) * al[2 * rb + ((i >> 1) & 1)]);
+              tmem_st_frag<16>(at, o);
+            }
         }
       }
-      const float off = M == -INFINITY ? 0.f : kPfLift - M;
-      const uint64_t mul2v = pk(mul, mul), off2 = pk(off, off);
-      // the weights, rounded to binary16; the sum takes the rounded ones, so a
-      // weight's rounding cancels where it dominates its row
-      float l0 = 0.f, l1 = 0.f;
-      uint32_t pw[KC / 2];
-#pragma unroll
-      for (int i = 0; i < KC / 2; ++i) {
-        const float2 x = upk(fma2(pk(__uint_as_float(zr[(2 * i) >> 5][(2 * i) & 31]),
-                                     __uint_as_float(zr[(2 * i) >> 5][((2 * i) & 31) + 1])),
-                                  mul2v, off2));
-        const __half2 p = __floats2half2_rn(fast_exp2(x.x), fast_exp2(x.y));
-        l0 = add_h_f(__low2half(p), l0);
-        l1 = add_h_f(__high2half(p), l1);
-        pw[i] = h2_as_u32(p);
-      }
+      // the weights, rounded to binary16 once; their sum in binary32
       const uint32_t p_col = tmem + lane_base + C::P_COL + (j & 1) * C::P_STEP + k0 / 2;
-      if constexpr (KC == 64)
-        tmem_st32(p_col, pw);
-      else
-        tmem_st16(p_col, pw);
-      l += l0 + l1;
-      tmem_st_wait();
-      if (!waited) {
-        live = __all_sync(0xffffffffu, wait(&sh.pv, (j - 1) & 1));
-        if (!live) break;
+#pragma unroll
+      for (int rb = 0; rb < 2; ++rb) {
+        uint32_t pw[2 * NI];
+        uint64_t l2[2] = {0ull, 0ull};
+        uint64_t mu[2], of[2];
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const float m1 = OPT ? 1.f : rs[2 * rb + hh];
+          mu[hh] = pk(m1, m1);
+          of[hh] = pk(off[2 * rb + hh], off[2 * rb + hh]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2 * NI; ++i) {  // column group i / 2, row half i % 2
+          const uint32_t* const z = &zr[rb][2 * i];
+          const float2 x = upk(fma2(pk(__uint_as_float(z[0]), __uint_as_float(z[1])), mu[i & 1],
+                                    of[i & 1]));
+          const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
+          l2[i & 1] = add2(l2[i & 1], pk(p0, p1));
+          pw[i] = h2_as_u32(__floats2half2_rn(p0, p1));
+        }
+        tmem_st_half<2 * NI>(p_col + ((uint32_t)(16 * rb) << 16), pw);
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const float2 f = upk(l2[hh]);
+          l[2 * rb + hh] += f.x + f.y;
+        }
       }
+      tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&sh.pf[j & 1]);
+      arrive(&sh.pf[j & 1]);
     }
+    float Mr = -INFINITY, lr = 0.f;  // of this thread's row in the last part
     if (ntile > 0) {
-      wait(&sh.pv, (ntile - 1) & 1);
-      tc_fence_after();
-      // the two halves' weight sums (the slot that tile ntile - 1 did not use)
-      float* const exj = ex + (ntile & 1) * 2 * kPfRows;
-      exj[wg * kPfRows + row] = l;
-      pf_pair_sync(qd);
-      l += exj[(wg ^ 1) * kPfRows + row];
+      wait(&sh.pv[(ntile - 1) & 3], ((ntile - 1) >> 2) & 1);
+      // the weight sums of the row's lanes and of the four warps
+      float* const exj = ex + (ntile & 1) * 4 * kPfRows;  // (not tile ntile - 1's slot)
+#pragma unroll
+      for (int rr = 0; rr < 4; ++rr) {
+        l[rr] += __shfl_xor_sync(0xffffffffu, l[rr], 1);
+        l[rr] += __shfl_xor_sync(0xffffffffu, l[rr], 2);
+        if (jl == 0) {
+          exj[wg * kPfRows + row0 + 8 * rr] = l[rr];
+          if (wg == 0) rst[row0 + 8 * rr].M = thr[rr] == -INFINITY ? -INFINITY : -off[rr];
+        }
+      }
+      pf_quarter_sync(qd);
+      Mr = rst[row].M;
+      lr = (exj[row] + exj[kPfRows + row]) + (exj[2 * kPfRows + row] + exj[3 * kPfRows + row]);
     }
     __syncwarp();
-    // ---- the thread's half of the row's result (V entered halved)
-    const int c0 = wg * C::HC;
+    // ---- the thread's channels of its row's result (V entered halved)
     if (a.part != nullptr) {
       float* dst = a.part + (R.row * a.splits + split) * (D + 4);
-      const bool some = ntile > 0 && M != -INFINITY;
+      const bool some = ntile > 0 && Mr != -INFINITY;
       if (ntile > 0) {
 #pragma unroll 1
         for (int c = c0; c < c0 + C::HC; c += 32) {
@@ -704,78 +819,109 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
         }
       }
       if (R.valid && wg == 0)
-        *reinterpret_cast<float2*>(dst + D) = make_float2(some ? M - kPfLift : -INFINITY, l);
+        *reinterpret_cast<float2*>(dst + D) = make_float2(some ? Mr : -INFINITY, lr);
     } else {
       __half* dst = a.out + R.row * D;
+      const float inv = lr > 0.f ? 2.f / lr : lr;  // (NaN stays)
+      const bool zero = Mr == -INFINITY;
       if (ntile > 0) {
-        const float inv = l > 0.f ? 2.f / l : l;  // (NaN stays)
-        const bool zero = M == -INFINITY;
         // normalised, back in channel order, then R^-1
 #pragma unroll 1
         for (int c = c0; c < c0 + C::HC; c += 32) {
-          uint32_t o[32], x[32];
+          uint32_t o[32];
+          float x[32];
           tmem_ld32(o_col + c, o);
           tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            x[(i & ~7) + pf_perm(i & 7)] =
-                zero ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
-          tmem_st32(o_col + c, x);
+            x[(i & ~7) + pf_perm(i & 7)] = zero ? 0.f : __uint_as_float(o[i]) * inv;
+          pf_rotate_in<true>(x, c, a.rot_kind, a.lgb, a.quat);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(x[i]);
+          tmem_st32(o_col + c, o);
         }
         tmem_st_wait();
-        pf_rotate<D, true>(o_col, wg, qd, a.rot_kind, a.lgb, a.quat);
+        pf_rotate_out<D>(o_col, wg, qd, a.rot_kind, a.lgb);
+      }
 #pragma unroll 1
-        for (int c = c0; c < c0 + C::HC; c += 32) {
-          uint32_t o[32];
+      for (int c = c0; c < c0 + C::HC; c += 32) {
+        uint32_t o[32];
+        if (ntile > 0) {
           tmem_ld32(o_col + c, o);
           tmem_ld_wait();
-          if (R.valid) {
+        } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = h2_as_u32(__floats2half2_rn(__uint_as_float(o[8 * k + 2 * e]),
-                                                   __uint_as_float(o[8 * k + 2 * e + 1])));
-              *reinterpret_cast<uint4*>(dst + c + 8 * k) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          }
-          __syncwarp();
+          for (int i = 0; i < 32; ++i) o[i] = 0u;
         }
-      } else if (R.valid) {
-#pragma unroll 1
-        for (int c = c0; c < c0 + C::HC; c += 8)
-          *reinterpret_cast<uint4*>(dst + c) = make_uint4(0u, 0u, 0u, 0u);
+        if (a.rot_kind == KVQ_ROT_HADAMARD_SIGNED) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            o[i] = __float_as_uint(__uint_as_float(o[i]) * __ldg(a.quat + c + i));
+        }
+        // whole rows leave through shared memory, coalesced (d = 128)
+        uint4* const st = C::QT ? reinterpret_cast<uint4*>(smem + C::QS_OFF + row * C::QS_PITCH + 2 * c)
+                                : reinterpret_cast<uint4*>(dst + c);
+        if (C::QT || R.valid) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = h2_as_u32(__floats2half2_rn(__uint_as_float(o[8 * k + 2 * e]),
+                                                 __uint_as_float(o[8 * k + 2 * e + 1])));
+            st[k] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        __syncwarp();
+      }
+      if (C::QT) {
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + qd) : "memory");
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int r = 8 * wg + 2 * k + (lane >> 4);  // row of the quarter
+          const int orow = __shfl_sync(0xffffffffu, (int)R.row, r);
+          const bool ok = __shfl_sync(0xffffffffu, (int)R.valid, r) != 0;
+          const uint4 u = *reinterpret_cast<const uint4*>(
+              smem + C::QS_OFF + (32 * qd + r) * C::QS_PITCH + 16 * (lane & 15));
+          if (ok) *reinterpret_cast<uint4*>(a.out + (int64_t)orow * D + 8 * (lane & 15)) = u;
+        }
       }
     }
     tc_fence_before();
-  } else if (wg < 4) {
-    // =========================== keys (warpgroup 2) and values (3) to binary16 operands
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    const bool isv = wg == 3;
+  } else if (wg < 6) {
+    // =========================== keys (warpgroup 4) and values (5) to binary16 operands
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    const bool isv = wg == 5;
     const int dt = tid & 127;
     const int key = dt % KT, part = dt / KT;  // 128 channels of one key
     const int P1 = (1 << a.lgP) - 1;
     const int32_t* bt = a.block_table + (int64_t)(a.shared_len >= 0 ? 0 : s) * a.bt_stride;
     const uint8_t* const codes = (isv ? a.v_codes : a.k_codes) + part * 64;
     const uint32_t* const params = isv ? a.v_params : a.k_params;
+    // (a tile is whole pages: the slot in its page is the key's own)
+    const uint32_t span = (uint32_t)(kv_hi - kv_lo);
+    const int tok0 = t0 * KT + key;
+    const int32_t* const bt0 = bt + (tok0 >> a.lgP);
+    const int pages = KT >> a.lgP;  // of a tile
     auto page_of = [&](int j) {
-      const int tok = (t0 + j) * KT + key;
-      return j < ntile && tok >= kv_lo && tok < kv_hi ? bt[tok >> a.lgP] : INT_MIN;  // not needed
+      return j < ntile && (uint32_t)(tok0 + j * KT - kv_lo) < span ? bt0[j * pages] : INT_MIN;  // not needed
     };
+    const int64_t row0 = ((int64_t)h << a.lgP) + (key & P1);
+    const uint8_t* const codes0 = codes + row0 * (D / 2);
+    const uint32_t* const params0 = params + row0;
+    const int64_t prows = (int64_t)a.H << a.lgP;  // rows of a page
     uint4 cr[2][4];         // codes of two tiles
     uint32_t pr[2];
-    bool bad[2];
-    auto load = [&](int page, int j, int st) {
-      const bool ok = page >= 0 && page < a.NP;
-      bad[st] = !ok && page != INT_MIN;
+    uint32_t bad = 0;       // bit st: the page of registers st is bad
+    auto load = [&](int page, int st) {
+      const bool ok = (uint32_t)page < (uint32_t)a.NP;
+      bad = (bad & ~(1u << st)) | ((uint32_t)(!ok && page != INT_MIN) << st);
       if (ok) {
-        const int tok = (t0 + j) * KT + key;
-        const int64_t row = (((int64_t)page * a.H + h) << a.lgP) + (tok & P1);
-        const uint4* src = reinterpret_cast<const uint4*>(codes + row * (D / 2));
+        const int64_t row = page * prows;
+        const uint4* src = reinterpret_cast<const uint4*>(codes0 + row * (D / 2));
 #pragma unroll
         for (int i = 0; i < 4; ++i) cr[st][i] = __ldg(src + i);
-        pr[st] = __ldg(params + row);
+        pr[st] = __ldg(params0 + row);
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) cr[st][i] = make_uint4(0u, 0u, 0u, 0u);
@@ -789,7 +935,12 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
     // tile j (registers st): stage, then load tile j + 2 with the page pg2
     auto step = [&](int j, int st, int pg2) {
       const int sl = NS == 2 ? (j & 1) : 0;
-      if (j >= NS && !wait(&empty[sl], NS == 2 ? ((j >> 1) - 1) & 1 : (j - 1) & 1)) return false;
+      if (j >= NS) {
+        // one warp polls for its warpgroup (polls of all eight took a tenth of
+        // the issue slots beside the softmax)
+        if ((warp & 3) == 0) wait(&empty[sl], NS == 2 ? ((j >> 1) - 1) & 1 : (j - 1) & 1);
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory");
+      }
       uint8_t* const dst = dst0 + sl * C::K_B;
       const uint32_t w4[16] = {
           cr[st][0].x, cr[st][0].y, cr[st][0].z, cr[st][0].w, cr[st][1].x, cr[st][1].y,
@@ -804,102 +955,105 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
         for (int w = 0; w < 16; ++w)
           *reinterpret_cast<uint4*>(dst + w * 128) = pf_codes_v(w4[w], s2, m2);
       } else {
-        float* ks = reinterpret_cast<float*>(smem + C::PAR_OFF) + (j & 3) * 2 * KT;
-        const uint32_t bm = __ballot_sync(0xffffffffu, bad[st]);
+        float* ks = reinterpret_cast<float*>(smem + C::PAR_OFF) + (j & 3) * 2 * KT +
+                    (key >> 1) * 4 + (key & 1);
+        const bool bd = (bad >> st) & 1u;
+        const uint32_t bm = __ballot_sync(0xffffffffu, bd);
         if (part == 0) {
           const float2 sm = __half22float2(u32_as_h2(pr[st]));
-          ks[key] = sm.x * a.scale2;
-          ks[KT + key] = fmaf(8.f, sm.x, sm.y) * a.scale2;
-          if (lane == 0) {
-            uint32_t* bw = reinterpret_cast<uint32_t*>(smem + C::BAD_OFF + (j & 3) * 16);
-            bw[key >> 5] = bm;
-            if (KT == 64) bw[2 + (key >> 5)] = 0u;
-          }
-          const int tok = (t0 + j) * KT + key;
-          if (bad[st] && h == 0 && ((tok & P1) == 0 || tok == kv_lo)) raise_flag(a.err, KVQ_ERRF_PAGE);
+          ks[0] = sm.x * a.scale2;
+          ks[2] = fmaf(-64.f, sm.x, sm.y) * a.scale2;  // (the operand holds 64 + c)
+          if (lane == 0)
+            reinterpret_cast<uint32_t*>(smem + C::BAD_OFF + (j & 3) * 16)[key >> 5] = bm;
+          if (bd && h == 0 && ((key & P1) == 0 || tok0 + j * KT == kv_lo)) raise_flag(a.err, KVQ_ERRF_PAGE);
         }
-        mbar_arrive(&sh.mf[j & 3]);
 #pragma unroll
         for (int w = 0; w < 16; ++w) *reinterpret_cast<uint4*>(dst + w * 128) = pf_codes_k(w4[w]);
       }
       fence_async_smem();
-      mbar_arrive(&full[sl]);
-      load(pg2, j + 2, st);
-      return true;
+      arrive(&full[sl]);
+      load(pg2, st);
     };
     if (ntile > 0) {
       int pga = page_of(0), pgb = page_of(1);
-      load(pga, 0, 0);
-      load(pgb, 1, 1);
+      load(pga, 0);
+      load(pgb, 1);
       pga = page_of(2);
       pgb = page_of(3);
       for (int j = 0; j < ntile; j += 2) {
-        if (!step(j, 0, pga)) break;
+        step(j, 0, pga);
         pga = page_of(j + 4);
-        if (j + 1 >= ntile || !step(j + 1, 1, pgb)) break;
+        if (j + 1 >= ntile) break;
+        step(j + 1, 1, pgb);
         pgb = page_of(j + 5);
       }
     }
   } else {
     // =========================== the issuing warp
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if (warp == 16 && ntile > 0) {
-    constexpr uint32_t idS = umma_idesc_f16(kPfRows, KT, 0);
-    constexpr uint32_t idO = umma_idesc_f16(kPfRows, D, 1);
-    const bool one = elect_one();
-    // keys: rows are keys, K-major; values: rows (the K dimension) are keys
-    const uint64_t kd0 = umma_desc_kmajor(smem_u32(smem + C::K_OFF), 128, C::GRP);
-    const uint64_t vd0 = umma_desc_kmajor(smem_u32(smem + C::V_OFF), C::GRP, 128);
-    const uint64_t qd = umma_desc_kmajor(smem_u32(smem), 128, C::GRP);
-    auto qk = [&](int j) {
-      const int sl = NS == 2 ? (j & 1) : 0;
-      const bool ok = wait(&sh.kf[sl], NS == 2 ? (j >> 1) & 1 : j & 1);
-      tc_fence_after();
-      const uint64_t kd = kd0 + (uint64_t)(sl * (C::K_B >> 4));
-      const uint32_t d = tmem + (j & 1) * KT;
-      if (one) {
+    if (warp == 24 && ntile > 0) {
+      constexpr uint32_t idS = umma_idesc_f16(kPfRows, KT, 0);
+      constexpr uint32_t idO = umma_idesc_f16(kPfRows, D, 1);
+      const bool one = elect_one();
+      // keys: rows are keys, K-major; values: rows (the K dimension) are keys
+      const uint64_t kd0 = umma_desc_kmajor(smem_u32(smem + C::K_OFF), 128, C::GRP);
+      const uint64_t vd0 = umma_desc_kmajor(smem_u32(smem + C::V_OFF), C::GRP, 128);
+      const uint64_t qd = umma_desc_kmajor(smem_u32(smem), 128, C::GRP);
+      wait(&sh.qf, 0);
+      // round i: the products P V of tile i - 2, then Q K^T of tile i
+      for (int i = 0; i < ntile + 2; ++i) {
+        if (i >= 2) {
+          const int j = i - 2;
+          const int sl = NS == 2 ? (j & 1) : 0;
+          wait(&sh.pf[j & 1], (j >> 1) & 1);
+          wait(&sh.vf[sl], NS == 2 ? (j >> 1) & 1 : j & 1);
+          tc_fence_after();
+          const uint32_t p = tmem + C::P_COL + (j & 1) * C::P_STEP, d = tmem + C::O_COL;
+          const uint64_t vd = vd0 + (uint64_t)(sl * (C::K_B >> 4));
+          if (one) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half)  // hi, then lo
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            if (C::QT)
-              umma_f16_ts(d, tmem + C::Q_COL + half * (D / 2) + 8 * k, kd + (uint64_t)(16 * k), idS,
-                          half + k > 0);
-            else
-              umma_f16_ss(d, qd + (uint64_t)(half * (C::Q_B >> 4) + 16 * k),
-                          kd + (uint64_t)(16 * k), idS, half + k > 0);
+            for (int k = 0; k < KT / 16; ++k)
+              umma_f16_ts(d, p + 8 * k, vd + (uint64_t)(k * (2 * C::GRP >> 4)), idO, j > 0 || k > 0);
+            umma_commit(&sh.pv[j & 3]);
+            umma_commit(&sh.ve[sl]);
           }
-        umma_commit(&sh.sf[j & 1]);
-        umma_commit(&sh.ke[sl]);
-      }
-      __syncwarp();
-      return ok;
-    };
-    bool ok = wait(&sh.qf, 0);
-    ok = ok && qk(0);
-    if (ntile > 1) ok = ok && qk(1);
-    for (int j = 0; j < ntile && ok; ++j) {
-      const int sl = NS == 2 ? (j & 1) : 0;
-      ok = wait(&sh.pf[j & 1], (j >> 1) & 1) && wait(&sh.vf[sl], NS == 2 ? (j >> 1) & 1 : j & 1);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t p = tmem + C::P_COL + (j & 1) * C::P_STEP, d = tmem + C::O_COL;
-      const uint64_t vd = vd0 + (uint64_t)(sl * (C::K_B >> 4));
-      if (one) {
+          __syncwarp();
+        }
+        if (i < ntile) {
+          const int sl = NS == 2 ? (i & 1) : 0;
+          wait(&sh.kf[sl], NS == 2 ? (i >> 1) & 1 : i & 1);
+          tc_fence_after();
+          const uint64_t kd = kd0 + (uint64_t)(sl * (C::K_B >> 4));
+          const uint32_t d = tmem + (i & 1) * KT;
+          if (one) {
 #pragma unroll
-        for (int k = 0; k < KT / 16; ++k)
-          umma_f16_ts(d, p + 8 * k, vd + (uint64_t)(k * (2 * C::GRP >> 4)), idO, j > 0 || k > 0);
-        umma_commit(&sh.pv);
-        umma_commit(&sh.ve[sl]);
+            for (int half = 0; half < 2; ++half)  // hi, then lo
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k) {
+                if (C::QT)
+                  umma_f16_ts(d, tmem + C::Q_COL + half * (D / 2) + 8 * k, kd + (uint64_t)(16 * k),
+                              idS, half + k > 0);
+                else
+                  umma_f16_ss(d, qd + (uint64_t)(half * (C::Q_B >> 4) + 16 * k),
+                              kd + (uint64_t)(16 * k), idS, half + k > 0);
+              }
+            umma_commit(&sh.sf[i & 1]);
+            umma_commit(&sh.ke[sl]);
+            // (an ordinary arrival hands on what the wait for the keys saw: the parameters)
+            mbar_arrive(&sh.sf[i & 1]);
+          }
+          __syncwarp();
+        }
       }
-      __syncwarp();
-      if (j + 2 < ntile) ok = qk(j + 2);
+      // nothing is in flight when tensor memory is given back
+      wait(&sh.pv[(ntile - 1) & 3], ((ntile - 1) >> 2) & 1);
     }
-    }
+    __syncwarp();
   }
   __syncthreads();
+  if (tid == 0 && sh.dead) raise_flag(a.err, KVQ_ERRF_TIMEOUT);
   tc_fence_after();
-  if (warp == 16) tmem_dealloc(tmem, kPfTmemCols);
+  if (warp == 24) tmem_dealloc(tmem, kPfTmemCols);
 }
 
 // ---------------------------------------------------------------------------
@@ -991,7 +1145,7 @@ __global__ void __launch_bounds__(128) prefill_merge_kernel(const PfMergeArgs m)
 
 static int log2i(int x) {
   int l = 0;
-  while ((1 << l) < x) ++l;
+  while (l < 30 && (1 << l) < x) ++l;
   return l;
 }
 
