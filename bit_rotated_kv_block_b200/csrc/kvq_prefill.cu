@@ -118,11 +118,24 @@ static_assert(sizeof(PfShared) <= 256, "shared state");
 
 }  // namespace
 
+// Division of 0 <= n < 2^31 by a fixed d >= 1 without a divide: with
+// 2^s >= d > 2^(s-1) and m = floor(2^32 (2^s - d) / d) + 1, n / d =
+// (floor(m n / 2^32) + n) >> s (Granlund and Montgomery, "Division by
+// invariant integers using multiplication", 1994).
+struct FastDiv {
+  uint32_t d, m, s;
+  __device__ __forceinline__ int div(int n) const {
+    return (int)((__umulhi(m, (uint32_t)n) + (uint32_t)n) >> s);
+  }
+};
+
 struct PrefillArgs {
+  FastDiv by_splits, by_heads, by_seqs, by_group;
   int S, T, Hq, H, G, lgP, NP, bt_stride, max_seq_len, max_q, mtiles, splits;
   int shared_len;  // < 0: prompt chunks; else the rows are the batch's sequences and the keys
                    // the first shared_len positions of block-table row 0
   int rot_kind, lgb;
+  float hscale;    // the Hadamard scale 1 / sqrt(b)
   float scale2;    // sm_scale log2(e)
   float capk, cap2;  // 2 / cap and cap log2(e); 0: no cap
   int window;      // 0: none
@@ -210,22 +223,11 @@ __device__ __forceinline__ void pf_cross16(uint32_t scr, int a, int b) {
 // The rotation of 32 channels [ch, ch + 32) as far as it stays inside them:
 // sign flips, butterflies below 32 and the scale, or the quaternion blocks.
 template <bool INV>
-__device__ __noinline__ void pf_rotate_quat(float (&x)[32], int ch, int rot_kind, const float* tbl) {
-  if (rot_kind == KVQ_ROT_QUAT) {
-    if (INV) quat_inv_regs<32>(x, tbl, ch); else quat_regs<32>(x, tbl, ch);
-  } else if (rot_kind == KVQ_ROT_QUAT_FAST) {
-    if (INV) quat_fast_inv_regs<32>(x, tbl, ch); else quat_fast_regs<32>(x, tbl, ch);
-  } else {
-    quat_mat_fly_regs<32, INV>(x, tbl, ch);
-  }
-}
-template <bool INV>
 __device__ __forceinline__ void pf_rotate_in(float (&x)[32], int ch, int rot_kind, int lgb,
-                                             const float* tbl) {
+                                             float cb, const float* tbl) {
   if (rot_kind == KVQ_ROT_NONE) return;
   if (rot_kind == KVQ_ROT_HADAMARD || rot_kind == KVQ_ROT_HADAMARD_SIGNED) {
     const bool sgn = rot_kind == KVQ_ROT_HADAMARD_SIGNED;
-    const float cb = hadamard_scale(lgb);
     if (!INV && sgn) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) x[i] *= __ldg(tbl + ch + i);
@@ -235,7 +237,13 @@ __device__ __forceinline__ void pf_rotate_in(float (&x)[32], int ch, int rot_kin
     for (int i = 0; i < 32; ++i) x[i] *= cb;
     return;
   }
-  pf_rotate_quat<INV>(x, ch, rot_kind, tbl);
+  if (rot_kind == KVQ_ROT_QUAT) {
+    if (INV) quat_inv_regs<32>(x, tbl, ch); else quat_regs<32>(x, tbl, ch);
+  } else if (rot_kind == KVQ_ROT_QUAT_FAST) {
+    if (INV) quat_fast_inv_regs<32>(x, tbl, ch); else quat_fast_regs<32>(x, tbl, ch);
+  } else {
+    quat_mat_fly_regs<32, INV>(x, tbl, ch);
+  }
 }
 // The wider Hadamard stages of a row in D tensor-memory columns at `scr`, by
 // the row's four threads (w = 0..3); each stage's column pairs are dealt out
@@ -331,14 +339,14 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
 
   // ---- which rows: splits fastest, then KV heads, then sequences, then row
   // tiles from the last (the longest under a causal mask) to the first
-  int b = blockIdx.x;
-  const int split = b % a.splits;
-  b /= a.splits;
-  const int h = b % a.H;
-  b /= a.H;
-  const int nseq = a.shared_len >= 0 ? 1 : a.S;
-  const int s = b % nseq;
-  const int mt = a.mtiles - 1 - b / nseq;
+  const int b0 = blockIdx.x;
+  const int b1 = a.by_splits.div(b0);
+  const int b2 = a.by_heads.div(b1);
+  const int b3 = a.by_seqs.div(b2);
+  const int split = b0 - b1 * a.splits;
+  const int h = b1 - b2 * a.H;
+  const int s = b2 - b3 * (int)a.by_seqs.d;
+  const int mt = a.mtiles - 1 - b3;
 
   pdl_wait();
   pdl_trigger();
@@ -396,7 +404,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
       const int r = 32 * k + (tid >> 4);
       const int ri = (int)r0 + r;
       const bool ok = ri < rows;
-      const int i = ok ? ri / a.G : 0;
+      const int i = ok ? a.by_group.div(ri) : 0;
       const int hd = ok ? h * a.G + ri - i * a.G : 0;
       cp_async16_zf(smem + C::QS_OFF + r * C::QS_PITCH + 16 * (tid & 15),
                     a.q + (int64_t)(ok ? q0 + i : 0) * a.q_stride + (int64_t)hd * D + 8 * (tid & 15),
@@ -414,7 +422,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
     const int64_t ri = r0 + (tid & 127);
     R.valid = ri < rows;
     if (R.valid) {
-      const int i = (int)ri / a.G;
+      const int i = a.by_group.div((int)ri);
       R.tok = q0 + i;
       R.head = h * a.G + (int)ri - i * a.G;
       R.row = (int64_t)R.tok * a.Hq + R.head;
@@ -520,7 +528,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
         }
         if (cs != nullptr) rope_regs<32>(x, cs + c);
         __syncwarp();
-        pf_rotate_in<false>(x, c0 + c, a.rot_kind, a.lgb, a.quat);
+        pf_rotate_in<false>(x, c0 + c, a.rot_kind, a.lgb, a.hscale, a.quat);
         uint32_t r[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(x[i]);
@@ -835,7 +843,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
 #pragma unroll
           for (int i = 0; i < 32; ++i)
             x[(i & ~7) + pf_perm(i & 7)] = zero ? 0.f : __uint_as_float(o[i]) * inv;
-          pf_rotate_in<true>(x, c, a.rot_kind, a.lgb, a.quat);
+          pf_rotate_in<true>(x, c, a.rot_kind, a.lgb, a.hscale, a.quat);
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(x[i]);
           tmem_st32(o_col + c, o);
@@ -1149,6 +1157,14 @@ static int log2i(int x) {
   return l;
 }
 
+static FastDiv fast_div(uint32_t d) {
+  FastDiv f;
+  f.d = d;
+  f.s = (uint32_t)log2i((int)d);
+  f.m = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << f.s) - d)) / d + 1);
+  return f;
+}
+
 // Splits of the key tiles: enough CTAs for one per SM when the rows alone
 // give fewer (each split holds at least two key tiles).
 static PrefillPlan plan_rows(int D, int H, int64_t nseq, int64_t rows_per_seq, int64_t total_rows,
@@ -1177,7 +1193,11 @@ PrefillPlan prefill_plan(const kvq_cache_desc& d, int32_t S, int32_t Hq, int32_t
 }
 
 template <int D, bool OPT>
-static cudaError_t launch_prefill(const PrefillArgs& a, int grid, cudaStream_t st) {
+static cudaError_t launch_prefill(PrefillArgs a, int grid, cudaStream_t st) {
+  a.by_splits = fast_div((uint32_t)a.splits);
+  a.by_heads = fast_div((uint32_t)a.H);
+  a.by_seqs = fast_div(a.shared_len >= 0 ? 1u : (uint32_t)a.S);
+  a.by_group = fast_div((uint32_t)a.G);
   auto kern = prefill_kernel<D, OPT>;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PfCfg<D>::SMEM);
@@ -1195,6 +1215,7 @@ static void fill_args(PrefillArgs& a, const kvq_cache_desc& d, int32_t S, int32_
   a.lgP = log2i(d.page_size); a.NP = d.num_pages; a.bt_stride = bt_stride;
   a.max_seq_len = max_seq_len;
   a.rot_kind = d.rot_kind; a.lgb = log2i(d.rot_block);
+  a.hscale = hadamard_scale(a.lgb);
   a.scale2 = (float)((double)sm_scale * 1.4426950408889634074);
   a.capk = sc && sc->softcap > 0.f ? 2.f / sc->softcap : 0.f;
   a.cap2 = sc ? (float)((double)sc->softcap * 1.4426950408889634074) : 0.f;
