@@ -51,7 +51,9 @@ namespace kvq {
 
 namespace {
 
-constexpr int kPfThreads = 896;   // softmax 512, keys 128, values 128, the issuing warp's group
+constexpr int kPfNW = 2;                          // softmax warpgroups
+constexpr int kPfThreads = kPfNW * 128 + 3 * 128;  // and keys, values, the issuing warp's group
+constexpr int kPfSoft = kPfNW * 128;
 constexpr int kPfRows = 128;      // rows of a CTA
 constexpr uint32_t kPfTmemCols = 512;
 // A row's reference maximum moves only when a score exceeds it by more than
@@ -63,8 +65,8 @@ constexpr float kPfLift = 7.f;
 template <int D>
 struct PfCfg {
   static constexpr int KT = D == 128 ? 128 : 64;  // keys per tile
-  static constexpr int KC = KT / 4;               // keys of a tile per softmax warp
-  static constexpr int HC = D / 4;                // channels of a row per softmax thread
+  static constexpr int KC = KT / kPfNW;               // keys of a tile per softmax warp
+  static constexpr int HC = D / kPfNW;                // channels of a row per softmax thread
   static constexpr int GRP = D * 16;              // bytes of 8 rows (D / 8 core matrices)
   // The query operand: in tensor memory at d = 128 (hi, then lo); in shared
   // memory at d = 256, where O leaves no columns for it. A product with A in
@@ -187,7 +189,7 @@ __device__ __forceinline__ constexpr int pf_perm(int i) { return (i >> 1) + 4 * 
 // with the ordering of their tensor-memory accesses.
 __device__ __forceinline__ void pf_quarter_sync(int quarter) {
   tc_fence_before();
-  asm volatile("bar.sync %0, 128;" ::"r"(1 + quarter) : "memory");
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + quarter), "n"(32 * kPfNW) : "memory");
   tc_fence_after();
 }
 // The same barrier with a vote: whether `p` holds in any of its 128 threads.
@@ -196,10 +198,10 @@ __device__ __forceinline__ bool pf_quarter_any(int quarter, bool p) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 q, %1, 0;\n\t"
-      "bar.red.or.pred p, %2, 128, q;\n\t"
+      "bar.red.or.pred p, %2, %3, q;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)p), "r"(1 + quarter)
+      : "r"((uint32_t)p), "r"(1 + quarter), "n"(32 * kPfNW)
       : "memory");
   return r != 0;
 }
@@ -258,7 +260,7 @@ __device__ __forceinline__ void pf_rotate_out(uint32_t scr, int w, int quarter, 
     // the D / 2 column pairs of distance 2^lg, 16 at a time: pair group k
     // starts at column (k / g) 2^(lg + 1) + 16 (k % g), g = 2^lg / 16
 #pragma unroll 1
-    for (int k = w; k < D / 32; k += 4) {
+    for (int k = w; k < D / 32; k += kPfNW) {
       const int g = (1 << lg) >> 4;
       const int a = (k / g) * (2 << lg) + 16 * (k % g);
       pf_cross16(scr, a, a + (1 << lg));
@@ -383,25 +385,25 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
       mbar_init(&sh.vf[i], 4);
       mbar_init(&sh.ve[i], 1);
       mbar_init(&sh.sf[i], 2);
-      mbar_init(&sh.pf[i], 16);
+      mbar_init(&sh.pf[i], kPfSoft / 32);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       mbar_init(&sh.pv[i], 1);
     }
-    mbar_init(&sh.qf, 16);
+    mbar_init(&sh.qf, kPfSoft / 32);
     sh.dead = 0;
     mbar_fence_init();
   }
-  if (warp == 24) {
+  if (warp == kPfSoft / 32 + 8) {
     tmem_alloc(&sh.tmem, kPfTmemCols);
     tmem_relinquish();
   }
   // ---- the query rows' copies (d = 128: whole rows, coalesced, to shared memory)
-  if (C::QT && wg < 4) {
+  if (C::QT && wg < kPfNW) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int r = 32 * k + (tid >> 4);
+    for (int k = 0; k < 16 / kPfNW; ++k) {
+      const int r = 8 * kPfNW * k + (tid >> 4);
       const int ri = (int)r0 + r;
       const bool ok = ri < rows;
       const int i = ok ? a.by_group.div(ri) : 0;
@@ -418,7 +420,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
   R.valid = false;
   R.row = 0;
   R.tok = R.head = R.p = R.lo = R.hi = 0;
-  if (wg < 4) {
+  if (wg < kPfNW) {
     const int64_t ri = r0 + (tid & 127);
     R.valid = ri < rows;
     if (R.valid) {
@@ -491,9 +493,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
     if (lane == 0) mbar_arrive(bar);
   };
 
-  if (wg < 4) {
+  if (wg < kPfNW) {
     // =========================== softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPfNW == 2 ? 144 : 88));
     const int qd = warp & 3;                    // lane quarter of the warp
     const int row = tid & 127;
     const uint32_t lane_base = (uint32_t)(qd * 32) << 16;
@@ -502,7 +504,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
     float* const ex = reinterpret_cast<float*>(smem + C::EX_OFF);
     if (C::QT) {  // every query row is in shared memory
       cp_async_wait<0>();
-      asm volatile("bar.sync 7, 512;" ::: "memory");
+      asm volatile("bar.sync 7, %0;" ::"n"(kPfSoft) : "memory");
     }
     if (ntile > 0) {
       // ---- the query row: RoPE, rotation (O's columns as scratch), then hi + lo
@@ -546,9 +548,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
         for (int i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf(__uint_as_float(r[i])));
       }
       ex[wg * kPfRows + row] = amax;
-      asm volatile("bar.sync %0, 128;" ::"r"(1 + qd) : "memory");
-      amax = fmaxf(fmaxf(ex[row], ex[kPfRows + row]),
-                   fmaxf(ex[2 * kPfRows + row], ex[3 * kPfRows + row]));
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + qd), "n"(32 * kPfNW) : "memory");
+#pragma unroll
+      for (int k = 0; k < kPfNW; ++k) amax = fmaxf(amax, ex[k * kPfRows + row]);
       float mul, rs, qsum = 0.f;
       pf_query_scale(amax, mul, rs);
 #pragma unroll 1
@@ -583,7 +585,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
       pf_quarter_sync(qd);
       if (wg == 0) {
         rst[row].rs = rs;
-        rst[row].qsum = (qsum + ex[5 * kPfRows + row]) + (ex[6 * kPfRows + row] + ex[7 * kPfRows + row]);
+#pragma unroll
+        for (int k = 1; k < kPfNW; ++k) qsum += ex[(4 + k) * kPfRows + row];
+        rst[row].qsum = qsum;
       }
       pf_quarter_sync(qd);
     }
@@ -616,8 +620,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
       for (int rb = 0; rb < 2; ++rb) tmem_ld_frag<4 * NI>(s_col + ((uint32_t)(16 * rb) << 16), zr[rb]);
       const float4* ks = reinterpret_cast<const float4*>(smem + C::PAR_OFF) + (j & 3) * (KT / 2) +
                          k0 / 2 + jl;
-      const uint32_t bad = *reinterpret_cast<const uint32_t*>(smem + C::BAD_OFF + (j & 3) * 16 +
-                                                              4 * (k0 / 32));
+      const uint32_t* const bads =
+          reinterpret_cast<const uint32_t*>(smem + C::BAD_OFF + (j & 3) * 16) + k0 / 32;
+      const uint32_t bad = KC == 64 ? bads[0] | bads[1] : bads[0];
       const int base = (t0 + j) * KT + k0;
       tmem_ld_wait();
       // z / rs = s'_j dot + m'_j qsum
@@ -682,15 +687,16 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
         }
       }
       if (bad != 0u) {
-        const uint32_t bw = bad >> (k0 & 31);
 #pragma unroll
-        for (int i = 0; i < NI; ++i)
+        for (int i = 0; i < NI; ++i) {
+          const uint32_t bw = bads[i / 4] >> ((k0 & 31) + 8 * (i & 3) + 2 * jl);
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            if ((bw >> (8 * i + 2 * jl + e)) & 1u) {
+            if ((bw >> e) & 1u) {
               zr[0][4 * i + e] = zr[0][4 * i + 2 + e] = 0xff800000u;
               zr[1][4 * i + e] = zr[1][4 * i + 2 + e] = 0xff800000u;
             }
+        }
       }
       // row maxima: of the thread's columns, then of the row's four lanes
       float mx[4];
@@ -716,12 +722,13 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
           mx[rr] = fmaxf(mx[rr], __shfl_xor_sync(0xffffffffu, mx[rr], 2));
           if (jl == 0) exj[wg * kPfRows + row0 + 8 * rr] = mx[rr];
         }
-        asm volatile("bar.sync %0, 128;" ::"r"(1 + qd) : "memory");
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + qd), "n"(32 * kPfNW) : "memory");
         float al[4];
 #pragma unroll
         for (int rr = 0; rr < 4; ++rr) {
           const float* const e = exj + row0 + 8 * rr;
-          mx[rr] = fmaxf(fmaxf(e[0], e[kPfRows]), fmaxf(e[2 * kPfRows], e[3 * kPfRows]));
+#pragma unroll
+          for (int k = 0; k < kPfNW; ++k) mx[rr] = fmaxf(mx[rr], e[k * kPfRows]);
           const bool mv = mx[rr] > thr[rr];
           const float no = mv ? kPfLift - mx[rr] : off[rr];
           al[rr] = thr[rr] == -INFINITY ? 0.f : fast_exp2(no - off[rr]);
@@ -797,7 +804,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
       }
       pf_quarter_sync(qd);
       Mr = rst[row].M;
-      lr = (exj[row] + exj[kPfRows + row]) + (exj[2 * kPfRows + row] + exj[3 * kPfRows + row]);
+#pragma unroll
+      for (int k = 0; k < kPfNW; ++k) lr += exj[k * kPfRows + row];
     }
     __syncwarp();
     // ---- the thread's channels of its row's result (V entered halved)
@@ -883,10 +891,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
         __syncwarp();
       }
       if (C::QT) {
-        asm volatile("bar.sync %0, 128;" ::"r"(1 + qd) : "memory");
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + qd), "n"(32 * kPfNW) : "memory");
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int r = 8 * wg + 2 * k + (lane >> 4);  // row of the quarter
+        for (int k = 0; k < 16 / kPfNW; ++k) {
+          const int r = 32 / kPfNW * wg + 2 * k + (lane >> 4);  // row of the quarter
           const int orow = __shfl_sync(0xffffffffu, (int)R.row, r);
           const bool ok = __shfl_sync(0xffffffffu, (int)R.valid, r) != 0;
           const uint4 u = *reinterpret_cast<const uint4*>(
@@ -896,10 +904,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
       }
     }
     tc_fence_before();
-  } else if (wg < 6) {
+  } else if (wg < kPfNW + 2) {
     // =========================== keys (warpgroup 4) and values (5) to binary16 operands
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    const bool isv = wg == 5;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPfNW == 2 ? 72 : 56));
+    const bool isv = wg == kPfNW + 1;
     const int dt = tid & 127;
     const int key = dt % KT, part = dt / KT;  // 128 channels of one key
     const int P1 = (1 << a.lgP) - 1;
@@ -947,7 +955,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
         // one warp polls for its warpgroup (polls of all eight took a tenth of
         // the issue slots beside the softmax)
         if ((warp & 3) == 0) wait(&empty[sl], NS == 2 ? ((j >> 1) - 1) & 1 : (j - 1) & 1);
-        asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory");
+        asm volatile("bar.sync %0, 128;" ::"r"(5 + (int)isv) : "memory");
       }
       uint8_t* const dst = dst0 + sl * C::K_B;
       const uint32_t w4[16] = {
@@ -999,7 +1007,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
   } else {
     // =========================== the issuing warp
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if (warp == 24 && ntile > 0) {
+    if (warp == kPfSoft / 32 + 8 && ntile > 0) {
       constexpr uint32_t idS = umma_idesc_f16(kPfRows, KT, 0);
       constexpr uint32_t idO = umma_idesc_f16(kPfRows, D, 1);
       const bool one = elect_one();
@@ -1061,7 +1069,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
   __syncthreads();
   if (tid == 0 && sh.dead) raise_flag(a.err, KVQ_ERRF_TIMEOUT);
   tc_fence_after();
-  if (warp == 24) tmem_dealloc(tmem, kPfTmemCols);
+  if (warp == kPfSoft / 32 + 8) tmem_dealloc(tmem, kPfTmemCols);
 }
 
 // ---------------------------------------------------------------------------
