@@ -12,14 +12,12 @@
 //
 // Work split. One CTA per (sequence, KV head, 128 rows, split of the key
 // tiles), 25 warps with a role each:
-//  - 16 softmax warps: warp (w, q) takes a quarter w of a key tile's columns
-//    for the 32 rows of tensor-memory quarter q, as fragments (four rows per
-//    thread, a quarter of the columns each), so that a key's scale and offset
-//    are read once per four rows: with one row per thread those broadcast
-//    reads alone (128 x 128 x 8 bytes into registers) took 1024 cycles of a
-//    tile. The four warps of a quarter agree on the rare moves of a row's
-//    reference maximum by a barrier with a vote. Four warps per scheduler hide
-//    one another's latencies (two: 3800 cycles per tile and 128 rows).
+//  - 8 softmax warps of 16 rows each, which they read as fragments (two rows
+//    per thread, a quarter of the columns), so that a row's maximum stays in
+//    four lanes and a key's scale and offset are read once per two rows. (One
+//    row per thread: the broadcast reads of scale and offset, 128 x 128 x 8
+//    bytes into registers, took 1024 cycles of a tile. Rows shared by two
+//    warps: their agreement on the maximum took 340.)
 //  - 4 + 4 warps widen the packed keys and values of the next tiles to
 //    binary16 operands in shared memory, one key per thread, with the codes of
 //    two tiles ahead in registers.
@@ -40,6 +38,7 @@
 #include <cuda_runtime.h>
 
 #include <climits>
+#include <cstddef>
 #include <type_traits>
 
 #include "kvq_device.cuh"
@@ -65,7 +64,6 @@ constexpr float kPfLift = 7.f;
 template <int D>
 struct PfCfg {
   static constexpr int KT = D == 128 ? 128 : 64;  // keys per tile
-  static constexpr int KC = KT / kPfNW;               // keys of a tile per softmax warp
   static constexpr int HC = D / kPfNW;                // channels of a row per softmax thread
   static constexpr int GRP = D * 16;              // bytes of 8 rows (D / 8 core matrices)
   // The query operand: in tensor memory at d = 128 (hi, then lo); in shared
@@ -108,7 +106,6 @@ struct PfShared {
   uint64_t kf[2], ke[2];  // key stage filled / consumed
   uint64_t vf[2], ve[2];  // value stage filled / consumed
   uint64_t sf[2];   // S of tile j (buffer j & 1), and the parameters of its keys
-  uint64_t pf[2];   // P of tile j
   uint64_t pv[4];   // O holds tile j's product (slot j & 3)
   uint64_t qf;      // query operands staged
   uint32_t tmem;
@@ -181,6 +178,27 @@ __device__ __forceinline__ void pf_wait(uint32_t bar, uint32_t parity, volatile 
   *dead = 1;
 }
 
+// 2^x for a pair on the FMA pipe: n = round(x) by the magic sum, 2^(x - n) on
+// [-1/2, 1/2] by a degree-4 polynomial (fitted to the relative error, 2.6e-6;
+// the weights are rounded to 2^-12 next), 2^n added to the exponent field.
+// Arguments below -125 (masked scores among them) give 2^-125, which rounds
+// to 0. A quarter of a tile's exponentials go this way: all of them on the
+// special-function pipe take 1024 cycles of a tile.
+__device__ __forceinline__ float2 pf_exp2_fma(float2 x) {
+  const uint64_t v = pk(fmaxf(x.x, -125.f), fmaxf(x.y, -125.f));
+  const float mg = 12582912.f;  // 1.5 2^23
+  const uint64_t t = add2(v, pk(mg, mg));
+  const uint64_t f = sub2(v, sub2(t, pk(mg, mg)));
+  uint64_t p = fma2(f, pk(0.009570102207362652f, 0.009570102207362652f),
+                    pk(0.05591786280274391f, 0.05591786280274391f));
+  p = fma2(p, f, pk(0.240247443318367f, 0.240247443318367f));
+  p = fma2(p, f, pk(0.6931217908859253f, 0.6931217908859253f));
+  p = fma2(p, f, pk(0.9999992847442627f, 0.9999992847442627f));
+  const float2 tt = upk(t), pp = upk(p);
+  return make_float2(__int_as_float((__float_as_int(tt.x) << 23) + __float_as_int(pp.x)),
+                     __int_as_float((__float_as_int(tt.y) << 23) + __float_as_int(pp.y)));
+}
+
 // Channels are visited in the order 0 4 1 5 2 6 3 7 inside each group of 8
 // (the nibble pairs that one mask extracts) by every operand.
 __device__ __forceinline__ constexpr int pf_perm(int i) { return (i >> 1) + 4 * (i & 1); }
@@ -192,20 +210,6 @@ __device__ __forceinline__ void pf_quarter_sync(int quarter) {
   asm volatile("bar.sync %0, %1;" ::"r"(1 + quarter), "n"(32 * kPfNW) : "memory");
   tc_fence_after();
 }
-// The same barrier with a vote: whether `p` holds in any of its 128 threads.
-__device__ __forceinline__ bool pf_quarter_any(int quarter, bool p) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 q, %1, 0;\n\t"
-      "bar.red.or.pred p, %2, %3, q;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r)
-      : "r"((uint32_t)p), "r"(1 + quarter), "n"(32 * kPfNW)
-      : "memory");
-  return r != 0;
-}
-
 // One butterfly stage between columns [a, a + 16) and [b, b + 16) of a row.
 __device__ __forceinline__ void pf_cross16(uint32_t scr, int a, int b) {
   uint32_t x[16], y[16];
@@ -296,7 +300,7 @@ struct alignas(16) PfRowState {
   int lo, hi, p;    // interval and position
   float slope2;     // slope of the distance bias, base 2
   float rs, qsum;   // 2^-e of the scaled query, and its sum
-  float M, pad;     // at the end: reference exponent M - lift
+  float M, l;       // at the end: reference exponent M - lift and weight sum
 };
 static_assert(sizeof(PfRowState) == 32, "row state");
 
@@ -332,7 +336,7 @@ __device__ __forceinline__ uint4 pf_codes_v(uint32_t x, __half2 s2, __half2 m2) 
 template <int D, bool OPT>
 __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArgs a) {
   using C = PfCfg<D>;
-  constexpr int KT = C::KT, KC = C::KC, NS = C::NS;
+  constexpr int KT = C::KT, NS = C::NS;
   extern __shared__ __align__(1024) uint8_t smem[];
   PfShared& sh = *reinterpret_cast<PfShared*>(smem + C::BAR_OFF);
   PfRowState* const rst = reinterpret_cast<PfRowState*>(smem + C::ROW_OFF);
@@ -385,7 +389,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
       mbar_init(&sh.vf[i], 4);
       mbar_init(&sh.ve[i], 1);
       mbar_init(&sh.sf[i], 2);
-      mbar_init(&sh.pf[i], kPfSoft / 32);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -592,18 +595,19 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
       pf_quarter_sync(qd);
     }
 
-    // ---- four rows per thread: row rr at 32 qd + 8 rr + lane / 4,
-    // columns 8 i + 2 (lane % 4) + {0, 1} of the warp's KC keys
-    constexpr int NI = KC / 8;  // column groups
+    // ---- two rows per thread: row rr at 32 qd + 16 wg + 8 rr + lane / 4,
+    // columns 8 i + 2 (lane % 4) + {0, 1} of the key tile
+    constexpr int NI = KT / 8;   // column groups
+    constexpr int NB = NI / 8;   // of 8 groups: one fragment load each
     const int jl = lane & 3;
-    const int row0 = 32 * qd + (lane >> 2);
+    const int row0 = 32 * qd + 16 * wg + (lane >> 2);
     const int all_lo = sh.all_lo[qd], all_hi = sh.all_hi[qd];
-    const int k0 = wg * KC;  // the warp's keys of a tile: [k0, k0 + KC)
+    const uint32_t lanes16 = lane_base + ((uint32_t)(16 * wg) << 16);  // the warp's 16 rows
     // per row: the reference maximum M, kept as M + slack and as the exponent's
     // offset (lift - M; 0 before any score)
-    float thr[4], off[4], l[4], rs[4], qs[4];
+    float thr[2], off[2], l[2], rs[2], qs[2];
 #pragma unroll
-    for (int rr = 0; rr < 4; ++rr) {
+    for (int rr = 0; rr < 2; ++rr) {
       thr[rr] = -INFINITY;
       off[rr] = 0.f;
       l[rr] = 0.f;
@@ -611,27 +615,24 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
       qs[rr] = rst[row0 + 8 * rr].qsum;
     }
     for (int j = 0; j < ntile; ++j) {
-      const uint32_t s_col = tmem + lane_base + (j & 1) * KT + k0;
       wait(&sh.sf[j & 1], (j >> 1) & 1);
       tc_fence_after();
-      // zr[rb][4 i + e]: row rr = 2 rb + e / 2, column 8 i + 2 jl + e % 2
-      uint32_t zr[2][4 * NI];
+      // zr[i / 8][4 (i % 8) + 2 rr + e]: row rr, column 8 i + 2 jl + e
+      uint32_t zr[NB][32];
 #pragma unroll
-      for (int rb = 0; rb < 2; ++rb) tmem_ld_frag<4 * NI>(s_col + ((uint32_t)(16 * rb) << 16), zr[rb]);
-      const float4* ks = reinterpret_cast<const float4*>(smem + C::PAR_OFF) + (j & 3) * (KT / 2) +
-                         k0 / 2 + jl;
-      const uint32_t* const bads =
-          reinterpret_cast<const uint32_t*>(smem + C::BAD_OFF + (j & 3) * 16) + k0 / 32;
-      const uint32_t bad = KC == 64 ? bads[0] | bads[1] : bads[0];
-      const int base = (t0 + j) * KT + k0;
+      for (int nb = 0; nb < NB; ++nb)
+        tmem_ld_frag<32>(tmem + lanes16 + (j & 1) * KT + 64 * nb, zr[nb]);
+      const float4* ks = reinterpret_cast<const float4*>(smem + C::PAR_OFF) + (j & 3) * (KT / 2) + jl;
+      const uint32_t* const bads = reinterpret_cast<const uint32_t*>(smem + C::BAD_OFF + (j & 3) * 16);
+      const int base = (t0 + j) * KT;
       tmem_ld_wait();
       // z / rs = s'_j dot + m'_j qsum
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const float4 pv = ks[4 * i];
 #pragma unroll
-        for (int rr = 0; rr < 4; ++rr) {
-          uint32_t* z = &zr[rr >> 1][4 * i + 2 * (rr & 1)];
+        for (int rr = 0; rr < 2; ++rr) {
+          uint32_t* z = &zr[i >> 3][4 * (i & 7) + 2 * rr];
           const float2 f = upk(fma2(pk(__uint_as_float(z[0]), __uint_as_float(z[1])), pk(pv.x, pv.y),
                                     mul2(pk(pv.z, pv.w), pk(qs[rr], qs[rr]))));
           z[0] = __float_as_uint(f.x);
@@ -640,95 +641,80 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
       }
       if (OPT) {
 #pragma unroll
-        for (int rr = 0; rr < 4; ++rr) {
-          uint32_t* const z = &zr[rr >> 1][2 * (rr & 1)];  // elements 4 i + e
+        for (int rr = 0; rr < 2; ++rr) {
           if (a.capk > 0.f) {
             // cap tanh(z / cap) = cap (1 - 2 / (1 + e^(2 z / cap)))
             const float k = rs[rr] * a.capk;
 #pragma unroll
-            for (int i = 0; i < NI; ++i)
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                z[4 * i + e] = __float_as_uint(
-                    fmaf(fast_rcp(1.f + fast_exp2(__uint_as_float(z[4 * i + e]) * k)),
-                         -2.f * a.cap2, a.cap2));
+            for (int i = 0; i < 2 * NI; ++i) {
+              uint32_t& z = zr[i >> 4][4 * ((i >> 1) & 7) + 2 * rr + (i & 1)];
+              z = __float_as_uint(fmaf(fast_rcp(1.f + fast_exp2(__uint_as_float(z) * k)),
+                                       -2.f * a.cap2, a.cap2));
+            }
           } else {
 #pragma unroll
-            for (int i = 0; i < NI; ++i)
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                z[4 * i + e] = __float_as_uint(__uint_as_float(z[4 * i + e]) * rs[rr]);
+            for (int i = 0; i < 2 * NI; ++i) {
+              uint32_t& z = zr[i >> 4][4 * ((i >> 1) & 7) + 2 * rr + (i & 1)];
+              z = __float_as_uint(__uint_as_float(z) * rs[rr]);
+            }
           }
           if (a.alibi != nullptr) {
             const PfRowState& w = rst[row0 + 8 * rr];
             const float sl = w.slope2, d0 = (float)(base + 2 * jl - w.p);
 #pragma unroll
-            for (int i = 0; i < NI; ++i)
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                z[4 * i + e] = __float_as_uint(
-                    fmaf(-sl, fabsf(d0 + (float)(8 * i + e)), __uint_as_float(z[4 * i + e])));
+            for (int i = 0; i < 2 * NI; ++i) {
+              uint32_t& z = zr[i >> 4][4 * ((i >> 1) & 7) + 2 * rr + (i & 1)];
+              z = __float_as_uint(
+                  fmaf(-sl, fabsf(d0 + (float)(8 * (i >> 1) + (i & 1))), __uint_as_float(z)));
+            }
           }
         }
       }
       // positions outside the row's interval, and keys of a bad page
-      if (base < all_lo || base + KC > all_hi) {
+      if (base < all_lo || base + KT > all_hi) {
 #pragma unroll
-        for (int rr = 0; rr < 4; ++rr) {
-          uint32_t* const z = &zr[rr >> 1][2 * (rr & 1)];
+        for (int rr = 0; rr < 2; ++rr) {
           const PfRowState& w = rst[row0 + 8 * rr];
           const int lo = w.lo - base - 2 * jl;
           const uint32_t len = (uint32_t)(w.hi - w.lo);
 #pragma unroll
-          for (int i = 0; i < NI; ++i)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              if ((uint32_t)(8 * i + e - lo) >= len) z[4 * i + e] = 0xff800000u;
+          for (int i = 0; i < 2 * NI; ++i)
+            if ((uint32_t)(8 * (i >> 1) + (i & 1) - lo) >= len)
+              zr[i >> 4][4 * ((i >> 1) & 7) + 2 * rr + (i & 1)] = 0xff800000u;
         }
       }
-      if (bad != 0u) {
+      if ((KT == 128 ? bads[0] | bads[1] | bads[2] | bads[3] : bads[0] | bads[1]) != 0u) {
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-          const uint32_t bw = bads[i / 4] >> ((k0 & 31) + 8 * (i & 3) + 2 * jl);
+          const uint32_t bw = bads[i / 4] >> (8 * (i & 3) + 2 * jl);
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            if ((bw >> e) & 1u) {
-              zr[0][4 * i + e] = zr[0][4 * i + 2 + e] = 0xff800000u;
-              zr[1][4 * i + e] = zr[1][4 * i + 2 + e] = 0xff800000u;
-            }
+            if ((bw >> e) & 1u)
+              zr[i >> 3][4 * (i & 7) + e] = zr[i >> 3][4 * (i & 7) + 2 + e] = 0xff800000u;
         }
       }
       // row maxima: of the thread's columns, then of the row's four lanes
-      float mx[4];
+      float mx[2];
 #pragma unroll
-      for (int rr = 0; rr < 4; ++rr) {
-        const uint32_t* const z = &zr[rr >> 1][2 * (rr & 1)];
-        float m0 = fmaxf(__uint_as_float(z[0]), __uint_as_float(z[1]));
+      for (int rr = 0; rr < 2; ++rr) {
+        float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-        for (int i = 1; i < NI; ++i)
-          m0 = max3(m0, __uint_as_float(z[4 * i]), __uint_as_float(z[4 * i + 1]));
-        mx[rr] = OPT ? m0 : m0 * rs[rr];
+        for (int i = 0; i < NI; i += 2) {
+          const uint32_t* const z = &zr[i >> 3][4 * (i & 7) + 2 * rr];
+          m0 = max3(m0, __uint_as_float(z[0]), __uint_as_float(z[1]));
+          m1 = max3(m1, __uint_as_float(z[4]), __uint_as_float(z[5]));
+        }
+        mx[rr] = fmaxf(m0, m1);
+        if (!OPT) mx[rr] *= rs[rr];
       }
-      bool move = false;
+      // a score exceeds its row's reference by more than the slack: the rows
+      // that do move theirs
+      if (__any_sync(0xffffffffu, mx[0] > thr[0] || mx[1] > thr[1])) {
+        float al[2];
 #pragma unroll
-      for (int rr = 0; rr < 4; ++rr) move = move || mx[rr] > thr[rr];
-      // a score of the quarter's rows exceeds its reference: all four warps
-      // take the rows' maxima over the whole tile
-      if (pf_quarter_any(qd, move)) {
-        float* const exj = ex + (j & 1) * 4 * kPfRows;
-#pragma unroll
-        for (int rr = 0; rr < 4; ++rr) {
+        for (int rr = 0; rr < 2; ++rr) {
           mx[rr] = fmaxf(mx[rr], __shfl_xor_sync(0xffffffffu, mx[rr], 1));
           mx[rr] = fmaxf(mx[rr], __shfl_xor_sync(0xffffffffu, mx[rr], 2));
-          if (jl == 0) exj[wg * kPfRows + row0 + 8 * rr] = mx[rr];
-        }
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + qd), "n"(32 * kPfNW) : "memory");
-        float al[4];
-#pragma unroll
-        for (int rr = 0; rr < 4; ++rr) {
-          const float* const e = exj + row0 + 8 * rr;
-#pragma unroll
-          for (int k = 0; k < kPfNW; ++k) mx[rr] = fmaxf(mx[rr], e[k * kPfRows]);
           const bool mv = mx[rr] > thr[rr];
           const float no = mv ? kPfLift - mx[rr] : off[rr];
           al[rr] = thr[rr] == -INFINITY ? 0.f : fast_exp2(no - off[rr]);
@@ -740,72 +726,66 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
           // (S of tile j implies the product of tile j - 2: the parity is not ambiguous)
           wait(&sh.pv[(j - 1) & 3], ((j - 1) >> 2) & 1);
           tc_fence_after();
-#pragma unroll
-          for (int rb = 0; rb < 2; ++rb)
 #pragma unroll 1
-            for (int c = 0; c < C::HC; c += 32) {
-              const uint32_t at = o_col + ((uint32_t)(16 * rb) << 16) + c0 + c;
-              uint32_t o[16];
-              tmem_ld_frag<16>(at, o);
-              tmem_ld_wait();
+          for (int c = 0; c < D; c += 32) {
+            const uint32_t at = tmem + lanes16 + C::O_COL + c;
+            uint32_t o[16];
+            tmem_ld_frag<16>(at, o);
+            tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 16; ++i)
-                o[i] = __float_as_uint(__uint_as_float(o[i]) * al[2 * rb + ((i >> 1) & 1)]);
-              tmem_st_frag<16>(at, o);
-            }
+            for (int i = 0; i < 16; ++i)
+              o[i] = __float_as_uint(__uint_as_float(o[i]) * al[(i >> 1) & 1]);
+            tmem_st_frag<16>(at, o);
+          }
         }
       }
       // the weights, rounded to binary16 once; their sum in binary32
-      const uint32_t p_col = tmem + lane_base + C::P_COL + (j & 1) * C::P_STEP + k0 / 2;
+      uint64_t l2[2] = {0ull, 0ull}, mu[2], of[2];
 #pragma unroll
-      for (int rb = 0; rb < 2; ++rb) {
-        uint32_t pw[2 * NI];
-        uint64_t l2[2] = {0ull, 0ull};
-        uint64_t mu[2], of[2];
+      for (int rr = 0; rr < 2; ++rr) {
+        const float m1 = OPT ? 1.f : rs[rr];
+        mu[rr] = pk(m1, m1);
+        of[rr] = pk(off[rr], off[rr]);
+      }
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const float m1 = OPT ? 1.f : rs[2 * rb + hh];
-          mu[hh] = pk(m1, m1);
-          of[hh] = pk(off[2 * rb + hh], off[2 * rb + hh]);
-        }
+      for (int nb = 0; nb < NB; ++nb) {
+        uint32_t pw[16];
 #pragma unroll
-        for (int i = 0; i < 2 * NI; ++i) {  // column group i / 2, row half i % 2
-          const uint32_t* const z = &zr[rb][2 * i];
+        for (int i = 0; i < 16; ++i) {  // column group i / 2, row i % 2
+          const uint32_t* const z = &zr[nb][2 * i];
           const float2 x = upk(fma2(pk(__uint_as_float(z[0]), __uint_as_float(z[1])), mu[i & 1],
                                     of[i & 1]));
-          const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
-          l2[i & 1] = add2(l2[i & 1], pk(p0, p1));
-          pw[i] = h2_as_u32(__floats2half2_rn(p0, p1));
+          const float2 p = (i & 3) == 3 ? pf_exp2_fma(x) : make_float2(fast_exp2(x.x), fast_exp2(x.y));
+          l2[i & 1] = add2(l2[i & 1], pk(p.x, p.y));
+          pw[i] = h2_as_u32(__floats2half2_rn(p.x, p.y));
         }
-        tmem_st_half<2 * NI>(p_col + ((uint32_t)(16 * rb) << 16), pw);
+        tmem_st_half<16>(tmem + lanes16 + C::P_COL + (j & 1) * C::P_STEP + 32 * nb, pw);
+      }
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const float2 f = upk(l2[hh]);
-          l[2 * rb + hh] += f.x + f.y;
-        }
+      for (int rr = 0; rr < 2; ++rr) {
+        const float2 f = upk(l2[rr]);
+        l[rr] += f.x + f.y;
       }
       tmem_st_wait();
       tc_fence_before();
-      arrive(&sh.pf[j & 1]);
+      // P is there: a named barrier that only the issuing warp waits at
+      asm volatile("bar.arrive %0, %1;" ::"r"(8 + (j & 1)), "n"(kPfSoft + 32) : "memory");
     }
     float Mr = -INFINITY, lr = 0.f;  // of this thread's row in the last part
     if (ntile > 0) {
       wait(&sh.pv[(ntile - 1) & 3], ((ntile - 1) >> 2) & 1);
-      // the weight sums of the row's lanes and of the four warps
-      float* const exj = ex + (ntile & 1) * 4 * kPfRows;  // (not tile ntile - 1's slot)
 #pragma unroll
-      for (int rr = 0; rr < 4; ++rr) {
+      for (int rr = 0; rr < 2; ++rr) {
         l[rr] += __shfl_xor_sync(0xffffffffu, l[rr], 1);
         l[rr] += __shfl_xor_sync(0xffffffffu, l[rr], 2);
         if (jl == 0) {
-          exj[wg * kPfRows + row0 + 8 * rr] = l[rr];
-          if (wg == 0) rst[row0 + 8 * rr].M = thr[rr] == -INFINITY ? -INFINITY : -off[rr];
+          rst[row0 + 8 * rr].l = l[rr];
+          rst[row0 + 8 * rr].M = thr[rr] == -INFINITY ? -INFINITY : -off[rr];
         }
       }
       pf_quarter_sync(qd);
       Mr = rst[row].M;
-#pragma unroll
-      for (int k = 0; k < kPfNW; ++k) lr += exj[k * kPfRows + row];
+      lr = rst[row].l;
     }
     __syncwarp();
     // ---- the thread's channels of its row's result (V entered halved)
@@ -1021,7 +1001,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
         if (i >= 2) {
           const int j = i - 2;
           const int sl = NS == 2 ? (j & 1) : 0;
-          wait(&sh.pf[j & 1], (j >> 1) & 1);
+          asm volatile("bar.sync %0, %1;" ::"r"(8 + (j & 1)), "n"(kPfSoft + 32) : "memory");
           wait(&sh.vf[sl], NS == 2 ? (j >> 1) & 1 : j & 1);
           tc_fence_after();
           const uint32_t p = tmem + C::P_COL + (j & 1) * C::P_STEP, d = tmem + C::O_COL;
