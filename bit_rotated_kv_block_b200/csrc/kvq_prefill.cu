@@ -614,7 +614,14 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
       rs[rr] = rst[row0 + 8 * rr].rs;
       qs[rr] = rst[row0 + 8 * rr].qsum;
     }
-    for (int j = 0; j < ntile; ++j) {
+    const bool mine = r0 + 32 * qd + 16 * wg < rows;
+    if (!mine) {  // a warp without rows only hands its (never read) weights on
+      for (int j = 0; j < ntile; ++j) {
+        wait(&sh.sf[j & 1], (j >> 1) & 1);
+        asm volatile("bar.arrive %0, %1;" ::"r"(8 + (j & 1)), "n"(kPfSoft + 32) : "memory");
+      }
+    }
+    for (int j = mine ? 0 : ntile; j < ntile; ++j) {
       wait(&sh.sf[j & 1], (j >> 1) & 1);
       tc_fence_after();
       // zr[i / 8][4 (i % 8) + 2 rr + e]: row rr, column 8 i + 2 jl + e
@@ -996,32 +1003,30 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
       const uint64_t vd0 = umma_desc_kmajor(smem_u32(smem + C::V_OFF), C::GRP, 128);
       const uint64_t qd = umma_desc_kmajor(smem_u32(smem), 128, C::GRP);
       wait(&sh.qf, 0);
-      // round i: the products P V of tile i - 2, then Q K^T of tile i
+      // round i: the products P V of tile i - 2, then Q K^T of tile i, issued
+      // back to back (their operands are waited for before P, the last to come)
       for (int i = 0; i < ntile + 2; ++i) {
-        if (i >= 2) {
-          const int j = i - 2;
-          const int sl = NS == 2 ? (j & 1) : 0;
+        const int j = i - 2;
+        const int sk = NS == 2 ? (i & 1) : 0, sv = NS == 2 ? (j & 1) : 0;
+        if (i < ntile) wait(&sh.kf[sk], NS == 2 ? (i >> 1) & 1 : i & 1);
+        if (j >= 0) {
+          wait(&sh.vf[sv], NS == 2 ? (j >> 1) & 1 : j & 1);
           asm volatile("bar.sync %0, %1;" ::"r"(8 + (j & 1)), "n"(kPfSoft + 32) : "memory");
-          wait(&sh.vf[sl], NS == 2 ? (j >> 1) & 1 : j & 1);
-          tc_fence_after();
-          const uint32_t p = tmem + C::P_COL + (j & 1) * C::P_STEP, d = tmem + C::O_COL;
-          const uint64_t vd = vd0 + (uint64_t)(sl * (C::K_B >> 4));
-          if (one) {
+        }
+        tc_fence_after();
+        if (one) {
+          if (j >= 0) {
+            const uint32_t p = tmem + C::P_COL + (j & 1) * C::P_STEP, d = tmem + C::O_COL;
+            const uint64_t vd = vd0 + (uint64_t)(sv * (C::K_B >> 4));
 #pragma unroll
             for (int k = 0; k < KT / 16; ++k)
               umma_f16_ts(d, p + 8 * k, vd + (uint64_t)(k * (2 * C::GRP >> 4)), idO, j > 0 || k > 0);
             umma_commit(&sh.pv[j & 3]);
-            umma_commit(&sh.ve[sl]);
+            umma_commit(&sh.ve[sv]);
           }
-          __syncwarp();
-        }
-        if (i < ntile) {
-          const int sl = NS == 2 ? (i & 1) : 0;
-          wait(&sh.kf[sl], NS == 2 ? (i >> 1) & 1 : i & 1);
-          tc_fence_after();
-          const uint64_t kd = kd0 + (uint64_t)(sl * (C::K_B >> 4));
-          const uint32_t d = tmem + (i & 1) * KT;
-          if (one) {
+          if (i < ntile) {
+            const uint64_t kd = kd0 + (uint64_t)(sk * (C::K_B >> 4));
+            const uint32_t d = tmem + (i & 1) * KT;
 #pragma unroll
             for (int half = 0; half < 2; ++half)  // hi, then lo
 #pragma unroll
@@ -1034,12 +1039,12 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
                               kd + (uint64_t)(16 * k), idS, half + k > 0);
               }
             umma_commit(&sh.sf[i & 1]);
-            umma_commit(&sh.ke[sl]);
+            umma_commit(&sh.ke[sk]);
             // (an ordinary arrival hands on what the wait for the keys saw: the parameters)
             mbar_arrive(&sh.sf[i & 1]);
           }
-          __syncwarp();
         }
+        __syncwarp();
       }
       // nothing is in flight when tensor memory is given back
       wait(&sh.pv[(ntile - 1) & 3], ((ntile - 1) >> 2) & 1);
