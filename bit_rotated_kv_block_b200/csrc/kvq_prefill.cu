@@ -284,15 +284,13 @@ __device__ __forceinline__ void pf_query_scale(float amax, float& mul, float& rs
   rs = amax > 0.f ? __int_as_float((127 - e) << 23) : 1.f;
 }
 
-// x0, x1 as binary16 hi + lo pairs; returns the sum of what they hold.
-__device__ __forceinline__ float pf_split(float x0, float x1, uint32_t& hi, uint32_t& lo) {
-  const __half2 hh = __floats2half2_rn(x0, x1);
+// x0 mul, x1 mul as binary16 hi + lo pairs (hi + lo is off by 2^-22 of the
+// value at most).
+__device__ __forceinline__ void pf_split(float x0, float x1, float mul, uint32_t& hi, uint32_t& lo) {
+  const __half2 hh = __floats2half2_rn(x0 * mul, x1 * mul);
   const float2 f = __half22float2(hh);
-  const __half2 ll = __floats2half2_rn(x0 - f.x, x1 - f.y);
-  const float2 g = __half22float2(ll);
   hi = h2_as_u32(hh);
-  lo = h2_as_u32(ll);
-  return (f.x + g.x) + (f.y + g.y);
+  lo = h2_as_u32(__floats2half2_rn(fmaf(x0, mul, -f.x), fmaf(x1, mul, -f.y)));
 }
 
 // What the softmax keeps per row in shared memory.
@@ -564,7 +562,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
           const int i = 8 * (k >> 2) + (k & 3);
-          qsum += pf_split(__uint_as_float(r[i]) * mul, __uint_as_float(r[i + 4]) * mul, hw[k], lw[k]);
+          const float x0 = __uint_as_float(r[i]), x1 = __uint_as_float(r[i + 4]);
+          qsum += x0 + x1;
+          pf_split(x0, x1, mul, hw[k], lw[k]);
         }
         if (C::QT) {
           const uint32_t qc = tmem + lane_base + C::Q_COL + (c0 + c) / 2;
@@ -584,10 +584,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
       if (C::QT) tmem_st_wait(); else fence_async_smem();
       tc_fence_before();
       arrive(&sh.qf);
-      ex[(4 + wg) * kPfRows + row] = qsum;
+      ex[(4 + wg) * kPfRows + row] = qsum * mul;
       pf_quarter_sync(qd);
       if (wg == 0) {
         rst[row].rs = rs;
+        qsum *= mul;
 #pragma unroll
         for (int k = 1; k < kPfNW; ++k) qsum += ex[(4 + k) * kPfRows + row];
         rst[row].qsum = qsum;
