@@ -178,25 +178,21 @@ __device__ __forceinline__ void pf_wait(uint32_t bar, uint32_t parity, volatile 
   *dead = 1;
 }
 
-// 2^x for a pair on the FMA pipe: n = round(x) by the magic sum, 2^(x - n) on
-// [-1/2, 1/2] by a degree-4 polynomial (fitted to the relative error, 2.6e-6;
-// the weights are rounded to 2^-12 next), 2^n added to the exponent field.
-// Arguments below -125 (masked scores among them) give 2^-125, which rounds
-// to 0. A quarter of a tile's exponentials go this way: all of them on the
-// special-function pipe take 1024 cycles of a tile.
-__device__ __forceinline__ float2 pf_exp2_fma(float2 x) {
-  const uint64_t v = pk(fmaxf(x.x, -125.f), fmaxf(x.y, -125.f));
-  const float mg = 12582912.f;  // 1.5 2^23
-  const uint64_t t = add2(v, pk(mg, mg));
-  const uint64_t f = sub2(v, sub2(t, pk(mg, mg)));
-  uint64_t p = fma2(f, pk(0.009570102207362652f, 0.009570102207362652f),
-                    pk(0.05591786280274391f, 0.05591786280274391f));
-  p = fma2(p, f, pk(0.240247443318367f, 0.240247443318367f));
-  p = fma2(p, f, pk(0.6931217908859253f, 0.6931217908859253f));
-  p = fma2(p, f, pk(0.9999992847442627f, 0.9999992847442627f));
-  const float2 tt = upk(t), pp = upk(p);
-  return make_float2(__int_as_float((__float_as_int(tt.x) << 23) + __float_as_int(pp.x)),
-                     __int_as_float((__float_as_int(tt.y) << 23) + __float_as_int(pp.y)));
+// cap tanh(u) (cap in base-2 units, cap2) for a pair with |u| <= kCapSeries:
+// an odd polynomial on the FMA pipe (fitted to the relative error, 5.8e-8).
+// Scores are far below the cap as a rule; the general form costs two
+// special-function results per score beside the exponential's one (a capped
+// chunk took 1.9 ms with it alone).
+constexpr float kCapSeries = 0.8f;
+__device__ __forceinline__ uint64_t pf_cap2(uint64_t u, uint64_t cap2) {
+  auto c = [](float x) { return pk(x, x); };
+  const uint64_t v = mul2(u, u);
+  uint64_t p = fma2(v, c(-0.00435529462993145f), c(0.019093291833996773f));
+  p = fma2(p, v, c(-0.053114309906959534f));
+  p = fma2(p, v, c(0.13321048021316528f));
+  p = fma2(p, v, c(-0.3333267569541931f));
+  p = fma2(p, v, c(0.9999999403953552f));
+  return mul2(mul2(u, cap2), p);
 }
 
 // Channels are visited in the order 0 4 1 5 2 6 3 7 inside each group of 8
@@ -648,32 +644,83 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
         }
       }
       if (OPT) {
+        // the pair of column group i in row rr
+        auto at = [&](int rr, int i) -> uint32_t* { return &zr[i >> 3][4 * (i & 7) + 2 * rr]; };
+        auto get = [&](int rr, int i) {
+          const uint32_t* z = at(rr, i);
+          return pk(__uint_as_float(z[0]), __uint_as_float(z[1]));
+        };
+        auto put = [&](int rr, int i, uint64_t v) {
+          const float2 f = upk(v);
+          uint32_t* z = at(rr, i);
+          z[0] = __float_as_uint(f.x);
+          z[1] = __float_as_uint(f.y);
+        };
+        if (a.capk > 0.f) {
+          // u = z / cap = z2 capk ln(2) / 2
+          bool small = true;
 #pragma unroll
-        for (int rr = 0; rr < 2; ++rr) {
-          if (a.capk > 0.f) {
-            // cap tanh(z / cap) = cap (1 - 2 / (1 + e^(2 z / cap)))
-            const float k = rs[rr] * a.capk;
+          for (int rr = 0; rr < 2; ++rr) {
+            const float ku = rs[rr] * a.capk * 0.34657359027997264f;
+            float m0 = 0.f, m1 = 0.f;
 #pragma unroll
-            for (int i = 0; i < 2 * NI; ++i) {
-              uint32_t& z = zr[i >> 4][4 * ((i >> 1) & 7) + 2 * rr + (i & 1)];
-              z = __float_as_uint(fmaf(fast_rcp(1.f + fast_exp2(__uint_as_float(z) * k)),
-                                       -2.f * a.cap2, a.cap2));
+            for (int i = 0; i < NI; ++i) {
+              const uint32_t* z = at(rr, i);
+              m0 = fmaxf(m0, fabsf(__uint_as_float(z[0])));
+              m1 = fmaxf(m1, fabsf(__uint_as_float(z[1])));
+            }
+            small = small && fmaxf(m0, m1) * ku <= kCapSeries;
+          }
+          if (__all_sync(0xffffffffu, small)) {
+            const uint64_t cp = pk(a.cap2, a.cap2);
+#pragma unroll
+            for (int rr = 0; rr < 2; ++rr) {
+              const float ku = rs[rr] * a.capk * 0.34657359027997264f;
+#pragma unroll
+              for (int i = 0; i < NI; ++i)
+                put(rr, i, pf_cap2(mul2(get(rr, i), pk(ku, ku)), cp));
             }
           } else {
+            // cap tanh(z / cap) = cap (1 - 2 / (1 + e^(2 z / cap)))
 #pragma unroll
-            for (int i = 0; i < 2 * NI; ++i) {
-              uint32_t& z = zr[i >> 4][4 * ((i >> 1) & 7) + 2 * rr + (i & 1)];
-              z = __float_as_uint(__uint_as_float(z) * rs[rr]);
+            for (int rr = 0; rr < 2; ++rr) {
+              const float k = rs[rr] * a.capk;
+#pragma unroll
+              for (int i = 0; i < NI; ++i) {
+                uint32_t* z = at(rr, i);
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  z[e] = __float_as_uint(
+                      fmaf(fast_rcp(1.f + fast_exp2(__uint_as_float(z[e]) * k)), -2.f * a.cap2,
+                           a.cap2));
+              }
             }
           }
-          if (a.alibi != nullptr) {
+        } else {
+#pragma unroll
+          for (int rr = 0; rr < 2; ++rr)
+#pragma unroll
+            for (int i = 0; i < NI; ++i) put(rr, i, mul2(get(rr, i), pk(rs[rr], rs[rr])));
+        }
+        if (a.alibi != nullptr) {
+#pragma unroll
+          for (int rr = 0; rr < 2; ++rr) {
             const PfRowState& w = rst[row0 + 8 * rr];
             const float sl = w.slope2, d0 = (float)(base + 2 * jl - w.p);
+            // (no later position than the query's, or none at all: no absolute value)
+            if (__all_sync(0xffffffffu, base + KT - 1 <= w.p)) {
 #pragma unroll
-            for (int i = 0; i < 2 * NI; ++i) {
-              uint32_t& z = zr[i >> 4][4 * ((i >> 1) & 7) + 2 * rr + (i & 1)];
-              z = __float_as_uint(
-                  fmaf(-sl, fabsf(d0 + (float)(8 * (i >> 1) + (i & 1))), __uint_as_float(z)));
+              for (int i = 0; i < NI; ++i)
+                put(rr, i, fma2(pk(sl, sl), add2(pk(d0, d0), pk(8.f * i, 8.f * i + 1.f)), get(rr, i)));
+            } else {
+#pragma unroll
+              for (int i = 0; i < NI; ++i) {
+                uint32_t* z = at(rr, i);
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  z[e] = __float_as_uint(
+                      fmaf(-sl, fabsf(d0 + (float)(8 * i + e)), __uint_as_float(z[e])));
+              }
             }
           }
         }
@@ -763,9 +810,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
           const uint32_t* const z = &zr[nb][2 * i];
           const float2 x = upk(fma2(pk(__uint_as_float(z[0]), __uint_as_float(z[1])), mu[i & 1],
                                     of[i & 1]));
-          const float2 p = (i & 3) == 3 ? pf_exp2_fma(x) : make_float2(fast_exp2(x.x), fast_exp2(x.y));
-          l2[i & 1] = add2(l2[i & 1], pk(p.x, p.y));
-          pw[i] = h2_as_u32(__floats2half2_rn(p.x, p.y));
+          const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
+          l2[i & 1] = add2(l2[i & 1], pk(p0, p1));
+          pw[i] = h2_as_u32(__floats2half2_rn(p0, p1));
         }
         tmem_st_half<16>(tmem + lanes16 + C::P_COL + (j & 1) * C::P_STEP + 32 * nb, pw);
       }
