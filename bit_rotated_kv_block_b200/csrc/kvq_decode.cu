@@ -94,6 +94,10 @@ struct DecodeArgs {
   float capk, cap2;  // 2 / cap and cap log2(e) (0: no cap)
   int window;        // positions seen, the query's included (0: all)
   int skip;          // positions below are left out (a prefix attended elsewhere)
+  // the kernel before this one shares only inputs with it (the prefix's part
+  // of the same call): run beside it, and wait for it at the end, so that the
+  // merge that waits for this kernel waits for both
+  int beside;
   const float* alibi;
   const int32_t* first_pos;
 };
@@ -227,7 +231,7 @@ __global__ void __launch_bounds__(kDecWarps * kWarp, D == 256 ? 2 : 3)
   extern __shared__ __align__(128) uint8_t smem[];
   // inputs may come from the previous kernel of the stream: nothing is read
   // before it has completed; the next launch may be scheduled right away
-  pdl_wait();
+  if (!SC || !a.beside) pdl_wait();
   pdl_trigger();
   const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
   const int r = lane >> 2, j = lane & 3;
@@ -925,6 +929,7 @@ __global__ void __launch_bounds__(kDecWarps * kWarp, D == 256 ? 2 : 3)
     float* dst = a.part + (base + (int64_t)hr * a.splits) * (D + 4);
     *reinterpret_cast<float2*>(dst + D) = make_float2(M, Lp);
   }
+  if (SC && a.beside) pdl_wait();
 }
 
 // ---------------------------------------------------------------------------
@@ -1184,12 +1189,13 @@ int decode_scored_split_launch(const kvq_cache_desc& d, int32_t S, int32_t Hq, c
                                const kvq_score_desc* sc, int32_t skip, const uint8_t* k_codes,
                                const void* k_params, const uint8_t* v_codes,
                                const void* v_params, void* workspace, int32_t* err,
-                               cudaStream_t st) {
+                               cudaStream_t st, bool beside) {
   const DecodePlan pl = decode_scored_plan(d, S, Hq, max_seq_len, skip, sc);
   DecodeArgs a = decode_args(d, pl, S, Hq, q, seq_lens, max_seq_len, block_table, bt_stride,
                              sm_scale, k_codes, k_params, v_codes, v_params, nullptr, workspace,
                              err);
   a.skip = skip;
+  a.beside = beside;
   if (sc != nullptr) {
     a.capk = sc->softcap > 0.f ? 2.f / sc->softcap : 0.f;
     a.cap2 = (float)((double)sc->softcap * 1.4426950408889634074);
@@ -1212,7 +1218,7 @@ int decode_scored_launch(const kvq_cache_desc& d, int32_t S, int32_t Hq, const v
   if (workspace == nullptr || workspace_bytes < pl.workspace) return KVQ_ERR_WORKSPACE;
   const int r = decode_scored_split_launch(d, S, Hq, q, seq_lens, max_seq_len, block_table,
                                            bt_stride, sm_scale, sc, 0, k_codes, k_params, v_codes,
-                                           v_params, workspace, err, st);
+                                           v_params, workspace, err, st, false);
   if (r != KVQ_OK) return r;
   return decode_merge_launch(d, S, Hq, pl.splits, pl.nhi, static_cast<float*>(workspace), out, st);
 }

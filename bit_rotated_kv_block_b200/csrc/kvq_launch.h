@@ -74,6 +74,8 @@ int decode_launch(const kvq_cache_desc& d, int32_t S, int32_t Hq, const void* q,
 // The scored form (INT4 pages): positions from `skip` on, inside the interval
 // the options leave. The split launch alone writes the partial results
 // (layout and plan as decode_launch's); decode_scored_launch merges them too.
+// beside: the launch before it on the stream belongs to the same call, writes
+// nothing that this one reads, and both run side by side.
 DecodePlan decode_scored_plan(const kvq_cache_desc& d, int32_t S, int32_t Hq, int32_t max_seq_len,
                               int32_t skip, const kvq_score_desc* sc);
 int decode_scored_split_launch(const kvq_cache_desc& d, int32_t S, int32_t Hq, const void* q,
@@ -82,7 +84,7 @@ int decode_scored_split_launch(const kvq_cache_desc& d, int32_t S, int32_t Hq, c
                                const kvq_score_desc* sc, int32_t skip, const uint8_t* k_codes,
                                const void* k_params, const uint8_t* v_codes,
                                const void* v_params, void* workspace, int32_t* err,
-                               cudaStream_t st);
+                               cudaStream_t st, bool beside);
 int decode_scored_launch(const kvq_cache_desc& d, int32_t S, int32_t Hq, const void* q,
                          const int32_t* seq_lens, int32_t max_seq_len,
                          const int32_t* block_table, int32_t bt_stride, float sm_scale,

@@ -1158,18 +1158,28 @@ __global__ void __launch_bounds__(128) prefill_merge_kernel(const PfMergeArgs m)
       Ls += ls;
       const uint32_t any = __ballot_sync(0xffffffffu, ml.x != -INFINITY);
       const int cnt = min(np - i0, kWarp);
-#pragma unroll 4
-      for (int k = 0; k < cnt; ++k) {
-        const float wk = __shfl_sync(0xffffffffu, w, k);
-        if (!((any >> k) & 1u)) continue;
-        const float4* p = reinterpret_cast<const float4*>(src + (int64_t)(i0 + k) * (D + 4) + lane * CPL);
+      // 8 rows in flight at a time
+      for (int k0 = 0; k0 < cnt; k0 += 8) {
+        float4 f[8][CPL / 4];
 #pragma unroll
-        for (int c = 0; c < CPL / 4; ++c) {
-          const float4 f = __ldcg(p + c);
-          x[4 * c] = fmaf(wk, f.x, x[4 * c]);
-          x[4 * c + 1] = fmaf(wk, f.y, x[4 * c + 1]);
-          x[4 * c + 2] = fmaf(wk, f.z, x[4 * c + 2]);
-          x[4 * c + 3] = fmaf(wk, f.w, x[4 * c + 3]);
+        for (int k = 0; k < 8; ++k) {
+          const bool in = k0 + k < cnt && ((any >> (k0 + k)) & 1u);
+          const float4* p =
+              reinterpret_cast<const float4*>(src + (int64_t)(i0 + k0 + k) * (D + 4) + lane * CPL);
+#pragma unroll
+          for (int c = 0; c < CPL / 4; ++c)
+            f[k][c] = in ? __ldcg(p + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float wk = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
+#pragma unroll
+          for (int c = 0; c < CPL / 4; ++c) {
+            x[4 * c] = fmaf(wk, f[k][c].x, x[4 * c]);
+            x[4 * c + 1] = fmaf(wk, f[k][c].y, x[4 * c + 1]);
+            x[4 * c + 2] = fmaf(wk, f[k][c].z, x[4 * c + 2]);
+            x[4 * c + 3] = fmaf(wk, f[k][c].w, x[4 * c + 3]);
+          }
         }
       }
     }
@@ -1352,7 +1362,7 @@ int shared_launch(const kvq_cache_desc& d, int32_t S, int32_t Hq, const void* q,
   }
   const int r = decode_scored_split_launch(d, S, Hq, q, seq_lens, max_seq_len, block_table,
                                            bt_stride, sm_scale, sc, prefix_len, k_codes, k_params,
-                                           v_codes, v_params, pb, err, st);
+                                           v_codes, v_params, pb, err, st, prefix_len > 0);
   if (r != KVQ_OK) return r;
   // (a window shrinks the own part's plan: the launch's own counts)
   const DecodePlan own = decode_scored_plan(d, S, Hq, max_seq_len, prefix_len, sc);

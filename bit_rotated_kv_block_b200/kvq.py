@@ -102,13 +102,28 @@ def lib():
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+# the current stream's handle without building a Stream object (3 us of a
+# call's host time), where this torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    return stream.cuda_stream
+
+
+def _on_current_device(t, name):
+    """The library launches on the current device: tensors of another one are
+    refused (call inside ``torch.cuda.device(...)``)."""
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
 
 
 def _check(fn, status):
@@ -267,6 +282,7 @@ def paged_prefill_attn(cache, q, q_start, max_q_len, seq_lens, max_seq_len, bloc
     S = int(seq_lens.numel())
     if q.stride(2) != 1 or q.stride(1) != d:
         raise ValueError("q rows of a token must be contiguous")
+    _on_current_device(q, "q")
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(d)
     if out is None:
@@ -292,6 +308,7 @@ def paged_decode_attn_scored(cache, q, seq_lens, max_seq_len, block_table, k_cod
     """``paged_decode_attn`` with scoring options (a ``Score``; its first_pos
     has one entry per sequence); same workspace."""
     S, Hq, d = q.shape
+    _on_current_device(q, "q")
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(d)
     if out is None:
@@ -324,6 +341,7 @@ def shared_prefix_decode_attn(cache, q, prefix_len, seq_lens, max_seq_len, block
     the batch); ``seq_lens`` are whole lengths. q: float16 CUDA [S][Hq][d];
     returns float16 [S][Hq][d]."""
     S, Hq, d = q.shape
+    _on_current_device(q, "q")
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(d)
     if out is None:
