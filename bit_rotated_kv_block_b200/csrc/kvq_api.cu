@@ -92,10 +92,14 @@ static int check_desc(const kvq_cache_desc* d) {
   return KVQ_OK;
 }
 
+// Positions and tile ends stay 32-bit sums in the entry points with options.
+constexpr int32_t kMaxPositions = INT32_MAX - 512;
+
 // Scoring options (NULL: none).
 static int check_score(const kvq_score_desc* sc) {
   if (sc == nullptr) return KVQ_OK;
-  if (!std::isfinite(sc->softcap) || sc->softcap < 0.f || sc->window < 0) return KVQ_ERR_INVALID_ARG;
+  if (!std::isfinite(sc->softcap) || (sc->softcap != 0.f && sc->softcap < 1e-6f) || sc->window < 0)
+    return KVQ_ERR_INVALID_ARG;
   if ((sc->alibi && !aligned4(sc->alibi)) || (sc->first_pos && !aligned4(sc->first_pos)) ||
       (sc->prefix_lens && !aligned4(sc->prefix_lens)))
     return KVQ_ERR_MISALIGNED;
@@ -223,7 +227,8 @@ int kvq_paged_prefill_attn(const kvq_cache_desc* desc, int32_t num_seqs, int32_t
   if (num_seqs < 1 || num_q_heads < 1 || num_tokens < 0 || max_q_len < 1 || max_seq_len < 0 ||
       bt_stride < 1 || !std::isfinite(sm_scale) || num_q_heads % desc->num_kv_heads != 0)
     return KVQ_ERR_INVALID_ARG;
-  if (desc->head_dim == 64 || desc->format != KVQ_FMT_INT4) return KVQ_ERR_UNSUPPORTED;
+  if (desc->head_dim == 64 || desc->format != KVQ_FMT_INT4 || max_seq_len > kMaxPositions)
+    return KVQ_ERR_UNSUPPORTED;
   if (num_tokens == 0) return KVQ_OK;
   if (!q || !q_start || !seq_lens || !block_table || !k_codes || !k_params || !v_codes ||
       !v_params || !out)
@@ -256,7 +261,7 @@ static int check_scored(const kvq_cache_desc* desc, int32_t num_seqs, int32_t nu
     return KVQ_ERR_INVALID_ARG;
   const int G = num_q_heads / desc->num_kv_heads;
   if (desc->format != KVQ_FMT_INT4 || desc->head_dim == 64 || G > 8 ||
-      (desc->head_dim == 256 && G > 4))
+      (desc->head_dim == 256 && G > 4) || max_seq_len > kMaxPositions)
     return KVQ_ERR_UNSUPPORTED;
   if (!q || !seq_lens || !block_table || !k_codes || !k_params || !v_codes || !v_params || !out)
     return KVQ_ERR_INVALID_ARG;

@@ -189,8 +189,16 @@ class Score:
                                                  for t in (alibi, first_pos, prefix_lens)))
 
 
-def _score(score):
-    return None if score is None else ctypes.byref(score.desc)
+def _score(score, q, seqs):
+    """The options' descriptor for queries ``q`` [rows][Hq][d] of ``seqs``
+    sequences; their tensors have to fit them."""
+    if score is None:
+        return None
+    for t, n, name in ((score.alibi, q.shape[1], "alibi"), (score.first_pos, q.shape[0], "first_pos"),
+                       (score.prefix_lens, seqs, "prefix_lens")):
+        if t is not None and (t.numel() != n or t.device != q.device):
+            raise ValueError(f"{name} must hold {n} entries on {q.device}")
+    return ctypes.byref(score.desc)
 
 
 def quantize_append(cache, k, v, token_seq, token_pos, block_table, k_codes, k_params, v_codes,
@@ -293,7 +301,7 @@ def paged_prefill_attn(cache, q, q_start, max_q_len, seq_lens, max_seq_len, bloc
     st = lib().kvq_paged_prefill_attn(ctypes.byref(cache.desc), S, Hq, T, _ptr(q),
                                       int(q.stride(0)), _ptr(q_start), int(max_q_len),
                                       _ptr(seq_lens), int(max_seq_len), _ptr(block_table),
-                                      int(block_table.shape[1]), float(sm_scale), _score(score),
+                                      int(block_table.shape[1]), float(sm_scale), _score(score, q, S),
                                       _ptr(k_codes), _ptr(k_params), _ptr(v_codes),
                                       _ptr(v_params), _ptr(out), _ptr(workspace),
                                       workspace.numel() * workspace.element_size(), _ptr(err),
@@ -319,7 +327,7 @@ def paged_decode_attn_scored(cache, q, seq_lens, max_seq_len, block_table, k_cod
     st = lib().kvq_paged_decode_attn_scored(ctypes.byref(cache.desc), S, Hq, _ptr(q),
                                             _ptr(seq_lens), int(max_seq_len), _ptr(block_table),
                                             int(block_table.shape[1]), float(sm_scale),
-                                            _score(score), _ptr(k_codes), _ptr(k_params),
+                                            _score(score, q, S), _ptr(k_codes), _ptr(k_params),
                                             _ptr(v_codes), _ptr(v_params), _ptr(out),
                                             _ptr(workspace),
                                             workspace.numel() * workspace.element_size(),
@@ -352,7 +360,7 @@ def shared_prefix_decode_attn(cache, q, prefix_len, seq_lens, max_seq_len, block
     st = lib().kvq_shared_prefix_decode_attn(ctypes.byref(cache.desc), S, Hq, _ptr(q),
                                              int(prefix_len), _ptr(seq_lens), int(max_seq_len),
                                              _ptr(block_table), int(block_table.shape[1]),
-                                             float(sm_scale), _score(score), _ptr(k_codes),
+                                             float(sm_scale), _score(score, q, S), _ptr(k_codes),
                                              _ptr(k_params), _ptr(v_codes), _ptr(v_params),
                                              _ptr(out), _ptr(workspace),
                                              workspace.numel() * workspace.element_size(),

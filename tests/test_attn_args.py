@@ -82,6 +82,8 @@ def test_prefill_refusals(L):
     assert prefill(L, desc(format=kvq.FMT_MXFP4)) == UNS
     assert prefill(L, desc(format=kvq.FMT_INT3)) == UNS
     assert prefill(L, desc(page_size=24)) == UNS
+    assert prefill(L, mx=2**31 - 1) == UNS          # positions stay 32-bit sums
+    assert prefill(L, T=2**30, mq=2**30, wsb=1 << 50) == UNS
     # few tokens over a long cache are split: the workspace is then needed
     assert prefill(L, mx=1 << 16, bts=1 << 12, wsb=64) == WSP
     assert prefill(L, mx=1 << 16, bts=1 << 12, ws=0) == WSP
@@ -99,7 +101,7 @@ def test_prefill_workspace_size(L):
 @pytest.mark.parametrize("call", [prefill, scored, shared])
 def test_score_options_are_checked(L, call):
     for bad in (score(softcap=-1.0), score(softcap=float("nan")), score(softcap=float("inf")),
-                score(window=-1)):
+                score(softcap=1e-9), score(window=-1)):
         assert call(L, sc=bad) == INV
     for bad in (score(alibi=GOOD + 2), score(first_pos=GOOD + 1)):
         assert call(L, sc=bad) == MIS
@@ -114,6 +116,7 @@ def test_decode_forms_refusals(L, call):
     assert call(L, desc(head_dim=256), Hq=40) == UNS
     assert call(L, desc(head_dim=64, rot_block=64)) == UNS
     assert call(L, desc(format=kvq.FMT_INT2)) == UNS
+    assert call(L, mx=2**31 - 1) == UNS
     assert call(L, sm=float("nan")) == INV
     for k in ("q", "lens", "bt", "pool", "out"):
         assert call(L, **{k: 0}) == INV, k
@@ -148,3 +151,16 @@ def test_score_object_checks_its_tensors():
         kvq.Score(first_pos=torch.zeros((4, 2), dtype=torch.int32)[:, 0])
     with pytest.raises(ValueError):
         kvq.Score(prefix_lens=torch.zeros(4, dtype=torch.int64))
+
+
+def test_score_tensors_have_to_fit_the_call():
+    import torch
+    q = torch.zeros((3, 8, 128))
+    assert kvq._score(None, q, 2) is None
+    kvq._score(kvq.Score(alibi=torch.zeros(8), first_pos=torch.zeros(3, dtype=torch.int32),
+                         prefix_lens=torch.zeros(2, dtype=torch.int32)), q, 2)
+    for bad in (kvq.Score(alibi=torch.zeros(7)), kvq.Score(first_pos=torch.zeros(2, dtype=torch.int32)),
+                kvq.Score(prefix_lens=torch.zeros(3, dtype=torch.int32)),
+                kvq.Score(alibi=torch.zeros(8, device="meta"))):
+        with pytest.raises(ValueError):
+            kvq._score(bad, q, 2)

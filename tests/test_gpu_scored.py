@@ -249,3 +249,58 @@ def test_chain_append_prefill_then_decode_steps_behind_a_shared_prefix():
         b.lens = [L] * S
         check(b, shared(b, qs, pre), qs, half=True)
         check(b, scored(b, qs, window=40, cap=20.0), qs, window=40, cap=20.0)
+
+
+def test_graphs_on_another_stream_match_eager():
+    """Captured calls (split and merge kernels, the prefix's part beside the
+    own part) replayed twice between other calls on the same workspace."""
+    b, q = batch([900, 700, 811], seed=13)
+    share(b, 640)
+    want_s, want_p = scored(b, q, cap=20.0, window=300), shared(b, q, 640, cap=20.0)
+    lens = b.i32(b.lens)
+    sc, sp = kvq.Score(20.0, 300), kvq.Score(20.0)
+    ws = torch.empty(kvq.decode_workspace_bytes(b.cache, 3, 8, 900) +
+                     kvq.shared_prefix_workspace_bytes(b.cache, 3, 8, 640, 900), dtype=torch.uint8,
+                     device="cuda")
+    o1, o2 = torch.zeros_like(want_s), torch.zeros_like(want_p)
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=st):
+        kvq.paged_decode_attn_scored(b.cache, q, lens, 900, b.table, b.kc, b.kp, b.vc, b.vp,
+                                     score=sc, out=o1, workspace=ws, stream=st)
+        kvq.shared_prefix_decode_attn(b.cache, q, 640, lens, 900, b.table, b.kc, b.kp, b.vc, b.vp,
+                                      score=sp, out=o2, workspace=ws, stream=st)
+    for _ in range(2):
+        o1.zero_(), o2.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o1, want_s) and torch.equal(o2, want_p)
+    # back to back on one stream and workspace, nothing waited for between
+    for _ in range(20):
+        kvq.shared_prefix_decode_attn(b.cache, q, 640, lens, 900, b.table, b.kc, b.kp, b.vc, b.vp,
+                                      score=sp, out=o2, workspace=ws)
+        kvq.paged_decode_attn_scored(b.cache, q, lens, 900, b.table, b.kc, b.kp, b.vc, b.vp,
+                                     score=sc, out=o1, workspace=ws)
+    torch.cuda.synchronize()
+    assert torch.equal(o1, want_s) and torch.equal(o2, want_p)
+
+
+def test_shared_prefix_seen_through_a_window_and_documents():
+    """Rows of which some see part of the prefix, some none of it."""
+    b, q = batch([700, 520, 900, 513], seed=14)
+    share(b, 512)
+    for kw in (dict(window=250), dict(window=1), dict(first=b.i32([100, 512, 600, 512])),
+               dict(first=b.i32([700, 0, 511, 513]))):
+        out = shared(b, q, 512, **kw)
+        check(b, out, q, half=True, **kw)
+    assert bool((out[0] == 0).all())       # its document begins behind it
+
+
+def test_tensors_of_another_device_are_refused():
+    b, q = batch([100], seed=15)
+    with pytest.raises(ValueError):
+        kvq.paged_decode_attn_scored(b.cache, q.cpu(), b.i32([100]), 100, b.table, b.kc, b.kp, b.vc,
+                                     b.vp)
+    with pytest.raises(ValueError):
+        scored(b, q, slopes=torch.zeros(3, device="cuda"))
