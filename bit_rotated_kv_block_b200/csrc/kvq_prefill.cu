@@ -81,12 +81,14 @@ struct PfCfg {
   static constexpr int BAD_OFF = PAR_OFF + 8 * KT * 4;  // 4 slots x 4 words
   static constexpr int EX_OFF = BAD_OFF + 64;           // exchange: 2 slots x 4 quarters x 128 floats
   static constexpr int ROW_OFF = EX_OFF + 2 * 4 * kPfRows * 4;  // PfRowState of 128 rows
-  // rows of the query (d = 128) as copied in, and of the output on its way
-  // out; 272-byte pitch: eight threads on the same channels of consecutive
-  // rows meet different banks
+  // Rows of the query as copied in, and of the output on its way out. The
+  // pitch lets eight threads on the same channels of consecutive rows meet
+  // different banks. At d = 256 they lie where the query operand will be (its
+  // rows are read before it is written) and was (at the end).
   static constexpr int QS_PITCH = 2 * D + 16;
-  static constexpr int QS_OFF = ROW_OFF + 32 * kPfRows;
-  static constexpr int BAR_OFF = QS_OFF + (QT ? kPfRows * QS_PITCH : 0);
+  static constexpr int QS_OFF = QT ? ROW_OFF + 32 * kPfRows : 0;
+  static constexpr int LPR = D / 8;  // 16-byte pieces of a row
+  static constexpr int BAR_OFF = ROW_OFF + 32 * kPfRows + (QT ? kPfRows * QS_PITCH : 0);
   static constexpr int SMEM = BAR_OFF + 256;
   // tensor-memory columns: S0, S1, O, then Q (d = 128) or P (d = 256)
   static constexpr int O_COL = 2 * KT;
@@ -396,17 +398,17 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
     tmem_alloc(&sh.tmem, kPfTmemCols);
     tmem_relinquish();
   }
-  // ---- the query rows' copies (d = 128: whole rows, coalesced, to shared memory)
-  if (C::QT && wg < kPfNW) {
+  // ---- the query rows' copies (whole rows, coalesced, to shared memory)
+  if (wg < kPfNW) {
 #pragma unroll
-    for (int k = 0; k < 16 / kPfNW; ++k) {
-      const int r = 8 * kPfNW * k + (tid >> 4);
+    for (int k = 0; k < kPfRows * C::LPR / kPfSoft; ++k) {
+      const int r = kPfSoft / C::LPR * k + tid / C::LPR, pc = tid % C::LPR;
       const int ri = (int)r0 + r;
       const bool ok = ri < rows;
       const int i = ok ? a.by_group.div(ri) : 0;
       const int hd = ok ? h * a.G + ri - i * a.G : 0;
-      cp_async16_zf(smem + C::QS_OFF + r * C::QS_PITCH + 16 * (tid & 15),
-                    a.q + (int64_t)(ok ? q0 + i : 0) * a.q_stride + (int64_t)hd * D + 8 * (tid & 15),
+      cp_async16_zf(smem + C::QS_OFF + r * C::QS_PITCH + 16 * pc,
+                    a.q + (int64_t)(ok ? q0 + i : 0) * a.q_stride + (int64_t)hd * D + 8 * pc,
                     ok ? 16u : 0u);
     }
     cp_async_commit();
@@ -499,24 +501,20 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
     const uint32_t o_col = tmem + lane_base + C::O_COL;
     const int c0 = wg * C::HC;                  // the thread's channels of its row
     float* const ex = reinterpret_cast<float*>(smem + C::EX_OFF);
-    if (C::QT) {  // every query row is in shared memory
-      cp_async_wait<0>();
-      asm volatile("bar.sync 7, %0;" ::"n"(kPfSoft) : "memory");
-    }
+    cp_async_wait<0>();  // every query row is in shared memory
+    asm volatile("bar.sync 7, %0;" ::"n"(kPfSoft) : "memory");
     if (ntile > 0) {
       // ---- the query row: RoPE, rotation (O's columns as scratch), then hi + lo
       const float* cs =
           a.rope != nullptr && R.valid && R.hi > 0 ? a.rope + (int64_t)R.p * D + c0 : nullptr;
       const uint4* src =
-          C::QT ? reinterpret_cast<const uint4*>(smem + C::QS_OFF + row * C::QS_PITCH + 2 * c0)
-                : reinterpret_cast<const uint4*>(a.q + (int64_t)R.tok * a.q_stride +
-                                                 (int64_t)R.head * D + c0);
+          reinterpret_cast<const uint4*>(smem + C::QS_OFF + row * C::QS_PITCH + 2 * c0);
 #pragma unroll 1
       for (int c = 0; c < C::HC; c += 32) {
         float x[32];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint4 u = C::QT || R.valid ? src[c / 8 + k] : make_uint4(0u, 0u, 0u, 0u);
+          const uint4 u = src[c / 8 + k];
           const uint32_t w4[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -534,6 +532,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
         tmem_st32(o_col + c0 + c, r);
       }
       tmem_st_wait();
+      // (d = 256: the operand goes where the rows were read)
+      if (!C::QT) asm volatile("bar.sync 7, %0;" ::"n"(kPfSoft) : "memory");
       pf_rotate_out<D>(o_col, wg, qd, a.rot_kind, a.lgb);
       float amax = 0.f;
 #pragma unroll 1
@@ -876,7 +876,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
       if (R.valid && wg == 0)
         *reinterpret_cast<float2*>(dst + D) = make_float2(some ? Mr : -INFINITY, lr);
     } else {
-      __half* dst = a.out + R.row * D;
       const float inv = lr > 0.f ? 2.f / lr : lr;  // (NaN stays)
       const bool zero = Mr == -INFINITY;
       if (ntile > 0) {
@@ -913,33 +912,28 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
           for (int i = 0; i < 32; ++i)
             o[i] = __float_as_uint(__uint_as_float(o[i]) * __ldg(a.quat + c + i));
         }
-        // whole rows leave through shared memory, coalesced (d = 128)
-        uint4* const st = C::QT ? reinterpret_cast<uint4*>(smem + C::QS_OFF + row * C::QS_PITCH + 2 * c)
-                                : reinterpret_cast<uint4*>(dst + c);
-        if (C::QT || R.valid) {
+        // whole rows leave through shared memory, coalesced
+        uint4* const st = reinterpret_cast<uint4*>(smem + C::QS_OFF + row * C::QS_PITCH + 2 * c);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t w[4];
+        for (int k = 0; k < 4; ++k) {
+          uint32_t w[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = h2_as_u32(__floats2half2_rn(__uint_as_float(o[8 * k + 2 * e]),
-                                                 __uint_as_float(o[8 * k + 2 * e + 1])));
-            st[k] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+          for (int e = 0; e < 4; ++e)
+            w[e] = h2_as_u32(__floats2half2_rn(__uint_as_float(o[8 * k + 2 * e]),
+                                               __uint_as_float(o[8 * k + 2 * e + 1])));
+          st[k] = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        __syncwarp();
       }
-      if (C::QT) {
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + qd), "n"(32 * kPfNW) : "memory");
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + qd), "n"(32 * kPfNW) : "memory");
+      constexpr int RPI = 32 / C::LPR;  // rows per instruction
 #pragma unroll
-        for (int k = 0; k < 16 / kPfNW; ++k) {
-          const int r = 32 / kPfNW * wg + 2 * k + (lane >> 4);  // row of the quarter
-          const int orow = __shfl_sync(0xffffffffu, (int)R.row, r);
-          const bool ok = __shfl_sync(0xffffffffu, (int)R.valid, r) != 0;
-          const uint4 u = *reinterpret_cast<const uint4*>(
-              smem + C::QS_OFF + (32 * qd + r) * C::QS_PITCH + 16 * (lane & 15));
-          if (ok) *reinterpret_cast<uint4*>(a.out + (int64_t)orow * D + 8 * (lane & 15)) = u;
-        }
+      for (int k = 0; k < 32 / kPfNW / RPI; ++k) {
+        const int r = 32 / kPfNW * wg + RPI * k + lane / C::LPR;  // row of the quarter
+        const int orow = __shfl_sync(0xffffffffu, (int)R.row, r);
+        const bool ok = __shfl_sync(0xffffffffu, (int)R.valid, r) != 0;
+        const uint4 u = *reinterpret_cast<const uint4*>(
+            smem + C::QS_OFF + (32 * qd + r) * C::QS_PITCH + 16 * (lane % C::LPR));
+        if (ok) *reinterpret_cast<uint4*>(a.out + (int64_t)orow * D + 8 * (lane % C::LPR)) = u;
       }
     }
     tc_fence_before();
