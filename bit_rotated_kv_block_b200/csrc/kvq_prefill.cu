@@ -782,15 +782,15 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
           wait(&sh.pv[(j - 1) & 3], ((j - 1) >> 2) & 1);
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
+          for (int c = 0; c < D; c += 64) {
             const uint32_t at = tmem + lanes16 + C::O_COL + c;
-            uint32_t o[16];
-            tmem_ld_frag<16>(at, o);
+            uint32_t o[32];
+            tmem_ld_frag<32>(at, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
+            for (int i = 0; i < 32; ++i)
               o[i] = __float_as_uint(__uint_as_float(o[i]) * al[(i >> 1) & 1]);
-            tmem_st_frag<16>(at, o);
+            tmem_st_frag<32>(at, o);
           }
         }
       }
@@ -1049,12 +1049,13 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
       const uint64_t vd0 = umma_desc_kmajor(smem_u32(smem + C::V_OFF), C::GRP, 128);
       const uint64_t qd = umma_desc_kmajor(smem_u32(smem), 128, C::GRP);
       wait(&sh.qf, 0);
-      // round i: the products P V of tile i - 2, then Q K^T of tile i, issued
-      // back to back (their operands are waited for before P, the last to come)
+      // Round i: the products P V of tile i - 2, then Q K^T of tile i. With two
+      // stages they are issued back to back, their operands waited for before P,
+      // the last to come; with one the keys of tile i are widened while P V runs.
       for (int i = 0; i < ntile + 2; ++i) {
         const int j = i - 2;
         const int sk = NS == 2 ? (i & 1) : 0, sv = NS == 2 ? (j & 1) : 0;
-        if (i < ntile) wait(&sh.kf[sk], NS == 2 ? (i >> 1) & 1 : i & 1);
+        if (NS == 2 && i < ntile) wait(&sh.kf[sk], (i >> 1) & 1);
         if (j >= 0) {
           wait(&sh.vf[sv], NS == 2 ? (j >> 1) & 1 : j & 1);
           asm volatile("bar.sync %0, %1;" ::"r"(8 + (j & 1)), "n"(kPfSoft + 32) : "memory");
@@ -1070,6 +1071,13 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
             umma_commit(&sh.pv[j & 3]);
             umma_commit(&sh.ve[sv]);
           }
+        }
+        __syncwarp();
+        if (NS == 1 && i < ntile) {
+          wait(&sh.kf[sk], i & 1);
+          tc_fence_after();
+        }
+        if (one) {
           if (i < ntile) {
             const uint64_t kd = kd0 + (uint64_t)(sk * (C::K_B >> 4));
             const uint32_t d = tmem + (i & 1) * KT;
