@@ -11,7 +11,7 @@
 // and out = R^-1 sum_j p_j v^_j with the online softmax in base 2.
 //
 // Work split. One CTA per (sequence, KV head, 128 rows, split of the key
-// tiles), 25 warps with a role each:
+// tiles); 17 of its warps have a role:
 //  - 8 softmax warps of 16 rows each, which they read as fragments (two rows
 //    per thread, a quarter of the columns), so that a row's maximum stays in
 //    four lanes and a key's scale and offset are read once per two rows. (One
@@ -24,6 +24,19 @@
 //  - 1 warp issues every tcgen05.mma: S = Q K^T, and O += P V with P read from
 //    tensor memory. S has two buffers, so one tile's softmax runs under the
 //    products of its neighbours.
+//
+// What bounds it (d = 128, one B200): a key tile of 128 takes 1.41 us, 2700
+// cycles at 1.92 GHz, of which the softmax warps' own chain (read S, scale,
+// maximum, exponentials, write P) is the whole: 24 products of 74 cycles take
+// 1776 (2130 with their hand-overs and no softmax at all), the exponentials
+// 1024 of the special-function pipe, all instructions 1290 issue slots per
+// scheduler. A CTA's first S comes 6 us after its start and its end 3 us after
+// the last product; at 4096 tokens that is a third of the time. Measured and
+// not kept: one CTA per SM walking over items with the next query copied
+// ahead (prompt 233 -> 234 us, few rows 25 -> 30 us), a tile per softmax
+// warpgroup in turn (1.82 us), a part of the exponentials on the FMA pipe
+// (0 to 2% slower), 16 softmax warps (1.66 us), binary16 scale and minimum
+// (1.46 us).
 //
 // Precision. Key codes enter as 64 + c, exact in binary16 (the offset costs
 // the binary32 sum three of its bits); the row's s and m are applied in
@@ -50,9 +63,10 @@ namespace kvq {
 
 namespace {
 
-constexpr int kPfNW = 2;                          // softmax warpgroups
-constexpr int kPfThreads = kPfNW * 128 + 3 * 128;  // and keys, values, the issuing warp's group
-constexpr int kPfSoft = kPfNW * 128;
+constexpr int kPfNW = 2;                   // softmax warpgroups
+constexpr int kPfSoft = kPfNW * 128;       // their threads
+constexpr int kPfThreads = kPfSoft + 384;  // and keys, values, the issuing warp's group
+constexpr int kPfIssue = kPfSoft / 32 + 8; // the issuing warp
 constexpr int kPfRows = 128;      // rows of a CTA
 constexpr uint32_t kPfTmemCols = 512;
 // A row's reference maximum moves only when a score exceeds it by more than
@@ -394,7 +408,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
     sh.dead = 0;
     mbar_fence_init();
   }
-  if (warp == kPfSoft / 32 + 8) {
+  if (warp == kPfIssue) {
     tmem_alloc(&sh.tmem, kPfTmemCols);
     tmem_relinquish();
   }
@@ -494,7 +508,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
 
   if (wg < kPfNW) {
     // =========================== softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPfNW == 2 ? 144 : 88));
+    // (register shares: 256 x 144 + 256 x 72 + 128 x 40 of the 640 x 96 at launch)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
     const int qd = warp & 3;                    // lane quarter of the warp
     const int row = tid & 127;
     const uint32_t lane_base = (uint32_t)(qd * 32) << 16;
@@ -938,8 +953,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
     }
     tc_fence_before();
   } else if (wg < kPfNW + 2) {
-    // =========================== keys (warpgroup 4) and values (5) to binary16 operands
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPfNW == 2 ? 72 : 56));
+    // =========================== keys (warpgroup 2) and values (3) to binary16 operands
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     const bool isv = wg == kPfNW + 1;
     const int dt = tid & 127;
     const int key = dt % KT, part = dt / KT;  // 128 channels of one key
@@ -1040,7 +1055,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
   } else {
     // =========================== the issuing warp
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if (warp == kPfSoft / 32 + 8 && ntile > 0) {
+    if (warp == kPfIssue && ntile > 0) {
       constexpr uint32_t idS = umma_idesc_f16(kPfRows, KT, 0);
       constexpr uint32_t idO = umma_idesc_f16(kPfRows, D, 1);
       const bool one = elect_one();
@@ -1108,7 +1123,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
   __syncthreads();
   if (tid == 0 && sh.dead) raise_flag(a.err, KVQ_ERRF_TIMEOUT);
   tc_fence_after();
-  if (warp == kPfSoft / 32 + 8) tmem_dealloc(tmem, kPfTmemCols);
+  if (warp == kPfIssue) tmem_dealloc(tmem, kPfTmemCols);
 }
 
 // ---------------------------------------------------------------------------
