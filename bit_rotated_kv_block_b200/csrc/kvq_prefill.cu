@@ -322,6 +322,21 @@ struct PfRow {
   int p, lo, hi;  // position and the interval it sees
 };
 
+// A sequence's n tokens from q0 on are rows of the call (n wraps to a negative
+// number or beyond max_q for ends that are not a range).
+__device__ __forceinline__ bool pf_range_ok(int q0, int n, int max_q, int T) {
+  return q0 >= 0 && n >= 0 && n <= max_q && q0 <= T - n;
+}
+
+// The value of the largest code of a row with halved (scale, minimum): finite
+// if the minimum and so, linear in the code, every value of the row is.
+__device__ __forceinline__ __half pf_value_top(__half2 hp) {
+  return __hfma(__float2half(15.f), __low2half(hp), __high2half(hp));
+}
+__device__ __forceinline__ __half2 pf_halved(uint32_t params) {
+  return __hmul2(u32_as_h2(params), __float2half2_rn(0.5f));
+}
+
 // Four bytes of codes (8 channels) as binary16 pairs in the operands' channel
 // order: 64 + c, exactly (the nibble OR-ed into bits 4-7 of the binary16 value
 // 64, 0x5400; seven logic operations and no arithmetic).
@@ -379,7 +394,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
     q0 = a.q_start[s];
     n = a.q_start[s + 1] - q0;
     L = a.seq_lens[s];
-    if (q0 < 0 || n < 0 || n > a.max_q || q0 > a.T - n) {  // not a range of the T rows: untouched
+    if (!pf_range_ok(q0, n, a.max_q, a.T)) {  // not a range of the T rows: untouched
       if (tid == 0 && h == 0 && mt == 0 && split == 0) raise_flag(a.err, KVQ_ERRF_SEQ);
       n = 0;
     }
@@ -854,7 +869,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
         l[rr] += __shfl_xor_sync(0xffffffffu, l[rr], 2);
         if (jl == 0) {
           rst[row0 + 8 * rr].l = l[rr];
-          rst[row0 + 8 * rr].M = thr[rr] == -INFINITY ? -INFINITY : -off[rr];
+          // (a row whose every score is NaN never moved its reference: off 0)
+          rst[row0 + 8 * rr].M = thr[rr] == -INFINITY && l[rr] == l[rr] ? -INFINITY : -off[rr];
         }
       }
       pf_quarter_sync(qd);
@@ -974,8 +990,12 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
     const uint8_t* const codes0 = codes + row0 * (D / 2);
     const uint32_t* const params0 = params + row0;
     const int64_t prows = (int64_t)a.H << a.lgP;  // rows of a page
+    // A value that is no finite number would turn every row of the tile to NaN
+    // (0 x NaN), also those that do not see it: it enters as zeros, and its key
+    // with a NaN scale, which reaches the rows that see it and no other.
+    const uint32_t* const vparams0 = a.v_params + row0;
     uint4 cr[2][4];         // codes of two tiles
-    uint32_t pr[2];
+    uint32_t pr[2], vr[2];  // parameters; key warps: the values' too
     uint32_t bad = 0;       // bit st: the page of registers st is bad
     auto load = [&](int page, int st) {
       const bool ok = (uint32_t)page < (uint32_t)a.NP;
@@ -986,10 +1006,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
 #pragma unroll
         for (int i = 0; i < 4; ++i) cr[st][i] = __ldg(src + i);
         pr[st] = __ldg(params0 + row);
+        vr[st] = isv ? 0u : __ldg(vparams0 + row);
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) cr[st][i] = make_uint4(0u, 0u, 0u, 0u);
-        pr[st] = 0u;
+        pr[st] = vr[st] = 0u;
       }
     };
     uint8_t* const dst0 = smem + (isv ? C::V_OFF : C::K_OFF) + (key >> 3) * C::GRP + part * 2048 +
@@ -1013,7 +1034,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
       if (isv) {
         // halved: the largest dequantized value (15 s + m, s rounded up) may
         // exceed the binary16 range by its rounding
-        const __half2 hp = __hmul2(u32_as_h2(pr[st]), __float2half2_rn(0.5f));
+        __half2 hp = pf_halved(pr[st]);
+        if (!(__habs(pf_value_top(hp)) <= __float2half(65504.f))) hp = __float2half2_rn(0.f);
         const __half2 s2 = __low2half2(hp), m2 = __high2half2(hp);
 #pragma unroll
         for (int w = 0; w < 16; ++w)
@@ -1025,7 +1047,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
         const uint32_t bm = __ballot_sync(0xffffffffu, bd);
         if (part == 0) {
           const float2 sm = __half22float2(u32_as_h2(pr[st]));
-          ks[0] = sm.x * a.scale2;
+          // (0 x top: NaN unless it is finite)
+          ks[0] = fmaf(0.f, __half2float(pf_value_top(pf_halved(vr[st]))), sm.x * a.scale2);
           ks[2] = fmaf(-64.f, sm.x, sm.y) * a.scale2;  // (the operand holds 64 + c)
           if (lane == 0)
             reinterpret_cast<uint32_t*>(smem + C::BAD_OFF + (j & 3) * 16)[key >> 5] = bm;
@@ -1140,16 +1163,31 @@ struct PfMergeArgs {
   const float* part_a;  // [rows][na][D + 4]
   const float* part_b;  // [rows][nb][D + 4]
   __half* out;
+  // prompt chunks: the rows that no valid range of q_start holds have no
+  // partials and are left as they are (NULL: every row has them)
+  const int32_t* q_start;
+  int S, T, Hq, max_q;
 };
 
 template <int D>
 __global__ void __launch_bounds__(128) prefill_merge_kernel(const PfMergeArgs m) {
   constexpr int CPL = D / 32;
-  pdl_wait();
-  pdl_trigger();
   const int lane = threadIdx.x % kWarp;
   const int64_t gw = (int64_t)blockIdx.x * 4 + threadIdx.x / kWarp;
-  if (gw >= m.rows) return;
+  // (an input of the call: complete since the launch before this one passed
+  // its own wait, which is before it let this one start)
+  bool held = m.q_start == nullptr;
+  if (!held) {
+    const int tok = (int)(gw / m.Hq);
+    for (int s = lane; s < m.S; s += kWarp) {
+      const int b = __ldcg(m.q_start + s), n = __ldcg(m.q_start + s + 1) - b;
+      held = held || (pf_range_ok(b, n, m.max_q, m.T) && tok >= b && tok - b < n);
+    }
+    held = __any_sync(0xffffffffu, held);
+  }
+  pdl_wait();
+  pdl_trigger();
+  if (gw >= m.rows || !held) return;
   float x[CPL];
 #pragma unroll
   for (int c = 0; c < CPL; ++c) x[c] = 0.f;
@@ -1312,11 +1350,16 @@ static cudaError_t launch_any(const PrefillArgs& a, int D, int grid, cudaStream_
 
 static cudaError_t launch_merge(const kvq_cache_desc& d, int64_t rows, int G, int na, int nb,
                                 int nhi, const float* pa, const float* pb, void* out,
-                                cudaStream_t st) {
+                                const PrefillArgs* rows_of, cudaStream_t st) {
   PfMergeArgs m;
   m.rows = (int)rows; m.G = G; m.rot_kind = d.rot_kind; m.lgb = log2i(d.rot_block);
   m.na = na; m.nb = nb; m.nhi = nhi; m.quat = d.quat; m.part_a = pa; m.part_b = pb;
   m.out = static_cast<__half*>(out);
+  m.q_start = rows_of ? rows_of->q_start : nullptr;
+  m.S = rows_of ? rows_of->S : 0;
+  m.T = rows_of ? rows_of->T : 0;
+  m.Hq = rows_of ? rows_of->Hq : 1;
+  m.max_q = rows_of ? rows_of->max_q : 0;
   const int grid = (int)((rows + 3) / 4);
   cudaError_t e = d.head_dim == 128 ? launch_pdl(prefill_merge_kernel<128>, grid, 128, 0, st, m)
                                     : launch_pdl(prefill_merge_kernel<256>, grid, 128, 0, st, m);
@@ -1344,7 +1387,8 @@ int prefill_launch(const kvq_cache_desc& d, int32_t S, int32_t Hq, int32_t T, co
   a.part = pl.splits > 1 ? static_cast<float*>(workspace) : nullptr;
   if (launch_any(a, d.head_dim, (int)pl.ctas, st) != cudaSuccess) return KVQ_ERR_CUDA;
   if (pl.splits > 1 &&
-      launch_merge(d, (int64_t)T * Hq, a.G, pl.splits, 0, 0, a.part, nullptr, out, st) != cudaSuccess)
+      launch_merge(d, (int64_t)T * Hq, a.G, pl.splits, 0, 0, a.part, nullptr, out, &a, st) !=
+          cudaSuccess)
     return KVQ_ERR_CUDA;
   return KVQ_OK;
 }
@@ -1391,7 +1435,7 @@ int shared_launch(const kvq_cache_desc& d, int32_t S, int32_t Hq, const void* q,
   // (a window shrinks the own part's plan: the launch's own counts)
   const DecodePlan own = decode_scored_plan(d, S, Hq, max_seq_len, prefix_len, sc);
   return launch_merge(d, (int64_t)S * Hq, Hq / d.num_kv_heads, pl.prefix.splits, own.splits,
-                      own.nhi, pa, pb, out, st) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+                      own.nhi, pa, pb, out, nullptr, st) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
 }  // namespace kvq

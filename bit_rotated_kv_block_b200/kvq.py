@@ -118,12 +118,42 @@ def _stream(stream):
     return stream.cuda_stream
 
 
-def _on_current_device(t, name):
-    """The library launches on the current device: tensors of another one are
-    refused (call inside ``torch.cuda.device(...)``)."""
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+def _ints(t, n, name, dev):
+    if t.dtype is not torch.int32 or t.numel() < n or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {n} entries on cuda:{dev}")
+
+
+def _fit(cache, q, seqs, seq_lens, block_table, kc, kp, vc, vp, out, out_dtype, workspace, err):
+    """Checks of the attention entry points with options: every tensor on the
+    current device (the library launches there; call inside
+    ``torch.cuda.device(...)`` for another), queries and outputs of the
+    geometry, index tensors int32 and contiguous. What the kernels would
+    misread is refused here. Returns q's shape and the device."""
+    dev = torch.cuda.current_device()
+    shape = q.shape
+    if q.dtype is not torch.float16 or len(shape) != 3 or shape[2] != cache.d:
+        raise ValueError(f"q must be float16 [rows][Hq][{cache.d}]")
+    if out is not None and (out.dtype is not out_dtype or out.shape != shape
+                            or not out.is_contiguous() or out.get_device() != dev):
+        raise ValueError(f"out must be a contiguous {out_dtype} tensor of q's shape on cuda:{dev}")
+    _ints(seq_lens, seqs, "seq_lens", dev)
+    if block_table.dim() != 2 or block_table.shape[0] < seqs:
+        raise ValueError("block_table must have a row per sequence")
+    _ints(block_table, 0, "block_table", dev)
+    if not (q.get_device() == kc.get_device() == kp.get_device() == vc.get_device()
+            == vp.get_device() == dev) or (workspace is not None and workspace.get_device() != dev) \
+            or (err is not None and err.get_device() != dev):
+        raise ValueError(f"q, pages, workspace and err must be on the current device, cuda:{dev}")
+    return shape, dev
+
+
+def _new(shape, dtype, q, stream):
+    """Output or workspace of a call on ``stream``: allocated on it, so that its
+    memory is neither taken from nor given to work that the call overlaps."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=q.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=q.device)
 
 
 def _check(fn, status):
@@ -184,9 +214,16 @@ class Score:
                             (prefix_lens, torch.int32, "prefix_lens")):
             if t is not None and (t.dtype != dt or not t.is_contiguous()):
                 raise ValueError(f"{name} must be a contiguous {dt} tensor")
-        self.alibi, self.first_pos, self.prefix_lens = alibi, first_pos, prefix_lens
+        if not 0 <= window < 2 ** 31:
+            raise ValueError("window must be in [0, 2^31)")
+        # (read-only: the descriptor holds their addresses)
+        self._alibi, self._first_pos, self._prefix_lens = alibi, first_pos, prefix_lens
         self.desc = ScoreDesc(softcap, window, *(None if t is None else t.data_ptr()
                                                  for t in (alibi, first_pos, prefix_lens)))
+
+    alibi = property(lambda self: self._alibi)
+    first_pos = property(lambda self: self._first_pos)
+    prefix_lens = property(lambda self: self._prefix_lens)
 
 
 def _score(score, q, seqs):
@@ -286,26 +323,25 @@ def paged_prefill_attn(cache, q, q_start, max_q_len, seq_lens, max_seq_len, bloc
     stride); ``q_start`` int32 [S + 1]: sequence s owns tokens
     [q_start[s], q_start[s + 1]), its last positions; returns float16
     [T][Hq][d]. ``score``: a ``Score`` (None: plain causal)."""
-    T, Hq, d = q.shape
-    S = int(seq_lens.numel())
-    if q.stride(2) != 1 or q.stride(1) != d:
+    S = seq_lens.numel()
+    (T, Hq, d), dev = _fit(cache, q, S, seq_lens, block_table, k_codes, k_params, v_codes, v_params,
+                           out, torch.float16, workspace, err)
+    _ints(q_start, S + 1, "q_start", dev)
+    if q.stride(2) != 1 or (Hq > 1 and q.stride(1) != d):
         raise ValueError("q rows of a token must be contiguous")
-    _on_current_device(q, "q")
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty((T, Hq, d), dtype=torch.float16, device=q.device)
+        out = _new((T, Hq, d), torch.float16, q, stream)
     if workspace is None:
         need = prefill_workspace_bytes(cache, S, Hq, T, max_q_len, max_seq_len)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    st = lib().kvq_paged_prefill_attn(ctypes.byref(cache.desc), S, Hq, T, _ptr(q),
-                                      int(q.stride(0)), _ptr(q_start), int(max_q_len),
-                                      _ptr(seq_lens), int(max_seq_len), _ptr(block_table),
-                                      int(block_table.shape[1]), float(sm_scale), _score(score, q, S),
-                                      _ptr(k_codes), _ptr(k_params), _ptr(v_codes),
-                                      _ptr(v_params), _ptr(out), _ptr(workspace),
-                                      workspace.numel() * workspace.element_size(), _ptr(err),
-                                      _stream(stream))
+        workspace = _new(max(need, 16), torch.uint8, q, stream)
+    st = lib().kvq_paged_prefill_attn(
+        ctypes.byref(cache.desc), S, Hq, T, q.data_ptr(), q.stride(0) if T > 1 else Hq * d,
+        q_start.data_ptr(), int(max_q_len), seq_lens.data_ptr(), int(max_seq_len),
+        block_table.data_ptr(), int(block_table.shape[1]), float(sm_scale), _score(score, q, S),
+        k_codes.data_ptr(), k_params.data_ptr(), v_codes.data_ptr(), v_params.data_ptr(),
+        out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _ptr(err), _stream(stream))
     _check("kvq_paged_prefill_attn", st)
     return out
 
@@ -315,23 +351,22 @@ def paged_decode_attn_scored(cache, q, seq_lens, max_seq_len, block_table, k_cod
                              sm_scale=None, err=None, stream=None):
     """``paged_decode_attn`` with scoring options (a ``Score``; its first_pos
     has one entry per sequence); same workspace."""
-    S, Hq, d = q.shape
-    _on_current_device(q, "q")
+    (S, Hq, d), _ = _fit(cache, q, q.shape[0], seq_lens, block_table, k_codes, k_params, v_codes,
+                         v_params, out, torch.float32, workspace, err)
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty((S, Hq, d), dtype=torch.float32, device=q.device)
+        out = _new((S, Hq, d), torch.float32, q, stream)
     if workspace is None:
         need = decode_workspace_bytes(cache, S, Hq, max_seq_len)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    st = lib().kvq_paged_decode_attn_scored(ctypes.byref(cache.desc), S, Hq, _ptr(q),
-                                            _ptr(seq_lens), int(max_seq_len), _ptr(block_table),
-                                            int(block_table.shape[1]), float(sm_scale),
-                                            _score(score, q, S), _ptr(k_codes), _ptr(k_params),
-                                            _ptr(v_codes), _ptr(v_params), _ptr(out),
-                                            _ptr(workspace),
-                                            workspace.numel() * workspace.element_size(),
-                                            _ptr(err), _stream(stream))
+        workspace = _new(max(need, 16), torch.uint8, q, stream)
+    st = lib().kvq_paged_decode_attn_scored(
+        ctypes.byref(cache.desc), S, Hq, q.data_ptr(), seq_lens.data_ptr(), int(max_seq_len),
+        block_table.data_ptr(), int(block_table.shape[1]), float(sm_scale), _score(score, q, S),
+        k_codes.data_ptr(), k_params.data_ptr(), v_codes.data_ptr(), v_params.data_ptr(),
+        out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _ptr(err), _stream(stream))
     _check("kvq_paged_decode_attn_scored", st)
     return out
 
@@ -348,23 +383,23 @@ def shared_prefix_decode_attn(cache, q, prefix_len, seq_lens, max_seq_len, block
     ``prefix_len`` tokens (pages taken from row 0 of the table, read once for
     the batch); ``seq_lens`` are whole lengths. q: float16 CUDA [S][Hq][d];
     returns float16 [S][Hq][d]."""
-    S, Hq, d = q.shape
-    _on_current_device(q, "q")
+    (S, Hq, d), _ = _fit(cache, q, q.shape[0], seq_lens, block_table, k_codes, k_params, v_codes,
+                         v_params, out, torch.float16, workspace, err)
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty((S, Hq, d), dtype=torch.float16, device=q.device)
+        out = _new((S, Hq, d), torch.float16, q, stream)
     if workspace is None:
         need = shared_prefix_workspace_bytes(cache, S, Hq, prefix_len, max_seq_len)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    st = lib().kvq_shared_prefix_decode_attn(ctypes.byref(cache.desc), S, Hq, _ptr(q),
-                                             int(prefix_len), _ptr(seq_lens), int(max_seq_len),
-                                             _ptr(block_table), int(block_table.shape[1]),
-                                             float(sm_scale), _score(score, q, S), _ptr(k_codes),
-                                             _ptr(k_params), _ptr(v_codes), _ptr(v_params),
-                                             _ptr(out), _ptr(workspace),
-                                             workspace.numel() * workspace.element_size(),
-                                             _ptr(err), _stream(stream))
+        workspace = _new(max(need, 16), torch.uint8, q, stream)
+    st = lib().kvq_shared_prefix_decode_attn(
+        ctypes.byref(cache.desc), S, Hq, q.data_ptr(), int(prefix_len), seq_lens.data_ptr(),
+        int(max_seq_len), block_table.data_ptr(), int(block_table.shape[1]), float(sm_scale),
+        _score(score, q, S), k_codes.data_ptr(), k_params.data_ptr(), v_codes.data_ptr(),
+        v_params.data_ptr(), out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _ptr(err),
+        _stream(stream))
     _check("kvq_shared_prefix_decode_attn", st)
     return out
 

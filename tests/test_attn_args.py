@@ -164,3 +164,13 @@ def test_score_tensors_have_to_fit_the_call():
                 kvq.Score(alibi=torch.zeros(8, device="meta"))):
         with pytest.raises(ValueError):
             kvq._score(bad, q, 2)
+
+
+def test_score_window_range_and_read_only_tensors():
+    import torch
+    for w in (-1, 2 ** 31, 2 ** 32 + 5):
+        with pytest.raises(ValueError):
+            kvq.Score(window=w)
+    sc = kvq.Score(alibi=torch.zeros(8))
+    with pytest.raises(AttributeError):
+        sc.alibi = torch.ones(8)     # the descriptor would go on holding the old address

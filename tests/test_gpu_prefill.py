@@ -227,3 +227,76 @@ def test_graph_replay_on_another_stream_matches():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_rows_of_no_sequence_stay_as_they_were_when_keys_are_split(d):
+    b = Batch([4000, 2500], [5, 3], d=d, tail=9, seed=11)
+    assert kvq.prefill_workspace_bytes(b.cache, 2, 8, b.T, 5, 4000) > 0
+    out = b.run(workspace=torch.full((1 << 24,), 0x3C, dtype=torch.uint8, device="cuda"))
+    b.check(out)
+    assert int(b.err.item()) == 0 and bool((out[8:] == 7.0).all())
+    b.q_start = [2, 7, 60]           # two rows before the first sequence; the second's is no range
+    out = b.run(workspace=torch.full((1 << 24,), 0x3C, dtype=torch.uint8, device="cuda"))
+    assert int(b.err.item()) == kvq.ERRF_SEQ
+    assert bool((out[:2] == 7.0).all()) and bool((out[7:] == 7.0).all())
+    assert bool((out[2:7] != 7.0).any())
+
+
+@pytest.mark.parametrize("word", [0x7C007C00, 0x7E007E00, 0x3C00FC00, 0x7BFF0000, 0x00007BFF])
+@pytest.mark.parametrize("key", [False, True], ids=["value", "key"])
+@pytest.mark.parametrize("d,lens,qn", [(128, [300], [300]), (256, [150], [150]), (128, [2500], [40])])
+def test_a_token_that_is_not_finite_reaches_only_the_queries_that_see_it(word, key, d, lens, qn):
+    # (scale, minimum) of one token: infinities, NaN, a minimum of -infinity,
+    # and finite pairs whose dequantized values leave the binary16 range
+    b = Batch(lens, qn, d=d, H=1, G=4, seed=12)
+    L, n = lens[0], qn[0]
+    at = L - n + 21                  # inside the first tiles of the chunk
+    keep = b.run(window=9)
+    pool = b.kp if key else b.vp
+    pool[int(b.table[0, at // 16]), 0, at % 16] = word
+    if not key:
+        b.vc[int(b.table[0, at // 16]), 0, at % 16] = 0xFF
+    out = b.run(window=9)
+    sees = torch.zeros(n, dtype=torch.bool, device="cuda")
+    sees[21:30] = True
+    assert torch.equal(out[~sees], keep[~sees])
+    if word in (0x7C007C00, 0x7E007E00) or (word == 0x3C00FC00 and not key):
+        assert bool(out[sees].isnan().all())
+    assert int(b.err.item()) == 0
+
+
+@pytest.mark.parametrize("lens,qn", [([300], [40]), ([4000], [5])])
+def test_a_query_that_is_not_a_number_stays_one(lens, qn):
+    b = Batch(lens, qn, seed=13)
+    keep = b.run()
+    b.q[2, 1, 5] = float("nan")
+    out = b.run()
+    assert bool(out[2, 1].isnan().all())
+    out[2, 1] = keep[2, 1]
+    assert torch.equal(out, keep)
+
+
+def test_tensors_that_would_be_misread_are_refused():
+    b = Batch([100, 60], [10, 20], seed=14)
+    qs, ls = b.i32(b.q_start), b.i32(b.lens)
+
+    def call(q=b.q, q_start=qs, lens=ls, table=b.table, out=None, vp=b.vp):
+        return kvq.paged_prefill_attn(b.cache, q, q_start, 20, lens, 100, table, b.kc, b.kp, b.vc,
+                                      vp, out=out)
+    want = call()
+    wide = torch.cat([b.table, b.table], 1)[:, :b.table.shape[1]]     # rows further apart
+    for kw in (dict(q=b.q.float()), dict(q=b.q.bfloat16()), dict(q=b.q[:, :, :64]),
+               dict(q=b.q.transpose(0, 1)), dict(q_start=qs.long()), dict(q_start=qs[:2]),
+               dict(q_start=qs.cpu()), dict(lens=ls.long()), dict(lens=ls.cpu()),
+               dict(table=b.table.long()), dict(table=b.table[:1]), dict(table=wide),
+               dict(table=b.table.cpu()), dict(vp=b.vp.cpu()), dict(out=want.float()),
+               dict(out=want[:5]), dict(out=want.transpose(0, 1).contiguous().transpose(0, 1))):
+        with pytest.raises(ValueError):
+            call(**kw)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    out = kvq.paged_prefill_attn(b.cache, b.q, qs, 20, ls, 100, b.table, b.kc, b.kp, b.vc, b.vp,
+                                 stream=st)     # its workspace and output live on that stream
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)

@@ -304,3 +304,45 @@ def test_tensors_of_another_device_are_refused():
                                      b.vp)
     with pytest.raises(ValueError):
         scored(b, q, slopes=torch.zeros(3, device="cuda"))
+
+
+def test_decode_tensors_that_would_be_misread_are_refused():
+    b, q = batch([100, 60], seed=16)
+    ls = b.i32(b.lens)
+    wide = torch.cat([b.table, b.table], 1)[:, :b.table.shape[1]]
+    odd = torch.empty((2, 9, 128), dtype=torch.float16, device="cuda")[:, :8]
+    for kw in (dict(q=q.float()), dict(q=odd), dict(q=q[..., :64]), dict(lens=ls.long()),
+               dict(lens=ls[:1]), dict(lens=ls.cpu()), dict(table=wide), dict(table=b.table[:1]),
+               dict(table=b.table.long()), dict(out=torch.empty_like(q).double())):
+        a = dict(q=q, lens=ls, table=b.table, out=None)
+        a.update(kw)
+        with pytest.raises(ValueError):
+            kvq.paged_decode_attn_scored(b.cache, a["q"], a["lens"], 100, a["table"], b.kc, b.kp,
+                                         b.vc, b.vp, out=a["out"])
+        with pytest.raises(ValueError):
+            kvq.shared_prefix_decode_attn(b.cache, a["q"], 32, a["lens"], 100, a["table"], b.kc,
+                                          b.kp, b.vc, b.vp, out=a["out"])
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_scored_masked_token_that_is_not_finite(d):
+    b, q = batch([700, 333], d=d, seed=17)
+    kw = dict(window=64)
+    keep = scored(b, q, **kw)
+    for s, L in enumerate(b.lens):
+        at = L - 66                  # just before the window, in a page it begins in or next to
+        b.kp[int(b.table[s, at // 16]), :, at % 16] = 0x7E007E00
+        b.vp[int(b.table[s, at // 16]), :, at % 16] = 0x7C007C00
+    assert torch.equal(scored(b, q, **kw), keep)
+
+
+def test_shared_masked_token_that_is_not_finite():
+    b, q = batch([310, 420, 555], seed=18)
+    share(b, 300)
+    kw = dict(window=200)
+    keep = shared(b, q, 300, **kw)
+    at = 290                         # seen by the first two sequences alone
+    b.kp[int(b.table[0, at // 16]), :, at % 16] = 0x7E007E00
+    b.vp[int(b.table[0, at // 16]), :, at % 16] = 0x7C007C00
+    out = shared(b, q, 300, **kw)
+    assert torch.equal(out[2], keep[2]) and bool(out[:2].isnan().all())
