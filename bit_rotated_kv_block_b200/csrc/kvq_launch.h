@@ -131,6 +131,7 @@ int decode_fp16_launch(const kvq_cache_desc& d, int32_t S, int32_t Hq, const voi
 // Attention of many query rows (prompt chunks; the shared prefix of a batch).
 struct PrefillPlan {
   int64_t mtiles;    // row tiles per (sequence, KV head)
+  bool pair;         // at most 64 rows: their weights enter as two binary16 parts
   int splits;        // splits of the key tiles
   int64_t ctas;
   size_t workspace;  // bytes of partial results (0: none)

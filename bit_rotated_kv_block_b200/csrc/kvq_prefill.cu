@@ -45,7 +45,8 @@
 // one binary16 it would cost |z| 2^-12 in every exponent, which for outlier
 // keys (|z| of 10 and more) is several times the output's own rounding. p and
 // v^ are rounded to binary16 once each (2^-12 relative on average, like the
-// binary16 output). All sums are binary32.
+// binary16 output); where a CTA has 64 rows at most, p enters
+// as hi + lo. All sums are binary32.
 
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -358,7 +359,9 @@ __device__ __forceinline__ uint4 pf_codes_v(uint32_t x, __half2 s2, __half2 m2) 
 
 // OPT: the cap and the distance bias are evaluated (their presence is still a
 // run-time, warp-uniform question).
-template <int D, bool OPT>
+// PAIR: at most 64 rows per (sequence, KV head). Row i is lane 32 (i / 16) +
+// i % 16 of its CTA, and 16 lanes on enters what binary16 left of its weights.
+template <int D, bool OPT, bool PAIR>
 __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArgs a) {
   using C = PfCfg<D>;
   constexpr int KT = C::KT, NS = C::NS;
@@ -427,12 +430,17 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
     tmem_alloc(&sh.tmem, kPfTmemCols);
     tmem_relinquish();
   }
+  // the row index of a lane of the tile (a number past every row: none)
+  auto row_of = [&](int r) {
+    if (!PAIR) return (int)r0 + r;
+    return (r & 16) ? INT_MAX : 16 * (r >> 5) + (r & 15);
+  };
   // ---- the query rows' copies (whole rows, coalesced, to shared memory)
   if (wg < kPfNW) {
 #pragma unroll
     for (int k = 0; k < kPfRows * C::LPR / kPfSoft; ++k) {
       const int r = kPfSoft / C::LPR * k + tid / C::LPR, pc = tid % C::LPR;
-      const int ri = (int)r0 + r;
+      const int ri = row_of(r);
       const bool ok = ri < rows;
       const int i = ok ? a.by_group.div(ri) : 0;
       const int hd = ok ? h * a.G + ri - i * a.G : 0;
@@ -449,12 +457,12 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
   R.row = 0;
   R.tok = R.head = R.p = R.lo = R.hi = 0;
   if (wg < kPfNW) {
-    const int64_t ri = r0 + (tid & 127);
+    const int ri = row_of(tid & 127);
     R.valid = ri < rows;
     if (R.valid) {
-      const int i = a.by_group.div((int)ri);
+      const int i = a.by_group.div(ri);
       R.tok = q0 + i;
-      R.head = h * a.G + (int)ri - i * a.G;
+      R.head = h * a.G + ri - i * a.G;
       R.row = (int64_t)R.tok * a.Hq + R.head;
       bool ok = seq_ok;
       if (a.shared_len >= 0) {
@@ -641,7 +649,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
       rs[rr] = rst[row0 + 8 * rr].rs;
       qs[rr] = rst[row0 + 8 * rr].qsum;
     }
-    const bool mine = r0 + 32 * qd + 16 * wg < rows;
+    const bool mine = row_of(32 * qd + 16 * wg) < rows;
     if (!mine) {  // a warp without rows only hands its (never read) weights on
       for (int j = 0; j < ntile; ++j) {
         wait(&sh.sf[j & 1], (j >> 1) & 1);
@@ -812,8 +820,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
           wait(&sh.pv[(j - 1) & 3], ((j - 1) >> 2) & 1);
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < D; c += 64) {
-            const uint32_t at = tmem + lanes16 + C::O_COL + c;
+          for (int c = 0; c < (PAIR ? 2 * D : D); c += 64) {
+            // (the lower part's lanes follow the weights' own)
+            const uint32_t at = tmem + lanes16 + C::O_COL + (c & (D - 1)) + (c >= D ? 16u << 16 : 0u);
             uint32_t o[32];
             tmem_ld_frag<32>(at, o);
             tmem_ld_wait();
@@ -826,7 +835,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
       }
       // the weights, rounded to binary16 once; their binary32 sum takes the
       // rounded ones, so that a weight's rounding cancels where it dominates its
-      // row (the result's error against float64 3.2e-4 -> 3.0e-4, a percent of time)
+      // row (the result's error against float64 3.2e-4 -> 3.0e-4, a percent of
+      // time). With lanes to spare (PAIR) they enter as two binary16 parts.
       uint64_t l2[2] = {0ull, 0ull}, mu[2], of[2];
 #pragma unroll
       for (int rr = 0; rr < 2; ++rr) {
@@ -836,7 +846,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
       }
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        uint32_t pw[16];
+        uint32_t pw[16], lw[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {  // column group i / 2, row i % 2
           const uint32_t* const z = &zr[nb][2 * i];
@@ -844,11 +854,19 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
                                     of[i & 1]));
           const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
           const __half2 ph = __floats2half2_rn(p0, p1);
-          const float2 ls = upk(l2[i & 1]);
-          l2[i & 1] = pk(add_h_f(__low2half(ph), ls.x), add_h_f(__high2half(ph), ls.y));
+          if (PAIR) {
+            l2[i & 1] = add2(l2[i & 1], pk(p0, p1));
+            const float2 f = __half22float2(ph);
+            lw[i] = h2_as_u32(__floats2half2_rn(p0 - f.x, p1 - f.y));
+          } else {
+            const float2 ls = upk(l2[i & 1]);
+            l2[i & 1] = pk(add_h_f(__low2half(ph), ls.x), add_h_f(__high2half(ph), ls.y));
+          }
           pw[i] = h2_as_u32(ph);
         }
-        tmem_st_half<16>(tmem + lanes16 + C::P_COL + (j & 1) * C::P_STEP + 32 * nb, pw);
+        const uint32_t at = tmem + lanes16 + C::P_COL + (j & 1) * C::P_STEP + 32 * nb;
+        tmem_st_half<16>(at, pw);
+        if (PAIR) tmem_st_half<16>(at + (16u << 16), lw);
       }
 #pragma unroll
       for (int rr = 0; rr < 2; ++rr) {
@@ -878,6 +896,15 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
       lr = rst[row].l;
     }
     __syncwarp();
+    // both parts of a row's result (the lower one 16 lanes on)
+    auto join = [&](uint32_t (&o)[32]) {
+      if (PAIR) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          o[i] = __float_as_uint(__uint_as_float(o[i]) +
+                                 __shfl_down_sync(0xffffffffu, __uint_as_float(o[i]), 16));
+      }
+    };
     // ---- the thread's channels of its row's result (V entered halved)
     if (a.part != nullptr) {
       float* dst = a.part + (R.row * a.splits + split) * (D + 4);
@@ -888,6 +915,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
           uint32_t o[32];
           tmem_ld32(o_col + c, o);
           tmem_ld_wait();
+          join(o);
           if (R.valid && some) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -917,6 +945,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
           float x[32];
           tmem_ld32(o_col + c, o);
           tmem_ld_wait();
+          join(o);
 #pragma unroll
           for (int i = 0; i < 32; ++i)
             x[(i & ~7) + pf_perm(i & 7)] = zero ? 0.f : __uint_as_float(o[i]) * inv;
@@ -1284,6 +1313,11 @@ static PrefillPlan plan_rows(int D, int H, int64_t nseq, int64_t rows_per_seq, i
   const int kt = D == 128 ? 128 : 64;
   pl.mtiles = (rows_per_seq + rt - 1) / rt;
   if (pl.mtiles < 1) pl.mtiles = 1;
+  // at most half a tile's rows: the free lanes take the weights' lower parts and
+  // the rows lie on all four schedulers. 8 sequences x 20 rows: 35.0 -> 34.2 us,
+  // error 3.1e-4 -> 2.9e-4; a 512-token prefix of 16 rows: 16.3 -> 17.1 us (two
+  // tiles per CTA, each with a second store), 3.0e-4 -> 2.7e-4
+  pl.pair = rows_per_seq <= rt / 2;
   const int64_t ctas = nseq * H * pl.mtiles;
   const int64_t tiles = (max_keys + kt - 1) / kt;
   const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
@@ -1303,13 +1337,13 @@ PrefillPlan prefill_plan(const kvq_cache_desc& d, int32_t S, int32_t Hq, int32_t
   return plan_rows(d.head_dim, d.num_kv_heads, S, (int64_t)max_q * G, (int64_t)T * Hq, max_seq_len);
 }
 
-template <int D, bool OPT>
+template <int D, bool OPT, bool PAIR>
 static cudaError_t launch_prefill(PrefillArgs a, int grid, cudaStream_t st) {
   a.by_splits = fast_div((uint32_t)a.splits);
   a.by_heads = fast_div((uint32_t)a.H);
   a.by_seqs = fast_div(a.shared_len >= 0 ? 1u : (uint32_t)a.S);
   a.by_group = fast_div((uint32_t)a.G);
-  auto kern = prefill_kernel<D, OPT>;
+  auto kern = prefill_kernel<D, OPT, PAIR>;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PfCfg<D>::SMEM);
   if (e != cudaSuccess) return e;
@@ -1342,10 +1376,17 @@ static void fill_args(PrefillArgs& a, const kvq_cache_desc& d, int32_t S, int32_
   a.err = err;
 }
 
-static cudaError_t launch_any(const PrefillArgs& a, int D, int grid, cudaStream_t st) {
+template <int D, bool OPT>
+static cudaError_t launch_pair(const PrefillArgs& a, bool pair, int grid, cudaStream_t st) {
+  return pair ? launch_prefill<D, OPT, true>(a, grid, st) : launch_prefill<D, OPT, false>(a, grid, st);
+}
+
+static cudaError_t launch_any(const PrefillArgs& a, int D, const PrefillPlan& pl, cudaStream_t st) {
   const bool opt = a.capk > 0.f || a.alibi != nullptr;
-  if (D == 128) return opt ? launch_prefill<128, true>(a, grid, st) : launch_prefill<128, false>(a, grid, st);
-  return opt ? launch_prefill<256, true>(a, grid, st) : launch_prefill<256, false>(a, grid, st);
+  const int grid = (int)pl.ctas;
+  if (D == 128)
+    return opt ? launch_pair<128, true>(a, pl.pair, grid, st) : launch_pair<128, false>(a, pl.pair, grid, st);
+  return opt ? launch_pair<256, true>(a, pl.pair, grid, st) : launch_pair<256, false>(a, pl.pair, grid, st);
 }
 
 static cudaError_t launch_merge(const kvq_cache_desc& d, int64_t rows, int G, int na, int nb,
@@ -1385,7 +1426,7 @@ int prefill_launch(const kvq_cache_desc& d, int32_t S, int32_t Hq, int32_t T, co
   a.mtiles = (int)pl.mtiles; a.splits = pl.splits; a.shared_len = -1;
   a.out = static_cast<__half*>(out);
   a.part = pl.splits > 1 ? static_cast<float*>(workspace) : nullptr;
-  if (launch_any(a, d.head_dim, (int)pl.ctas, st) != cudaSuccess) return KVQ_ERR_CUDA;
+  if (launch_any(a, d.head_dim, pl, st) != cudaSuccess) return KVQ_ERR_CUDA;
   if (pl.splits > 1 &&
       launch_merge(d, (int64_t)T * Hq, a.G, pl.splits, 0, 0, a.part, nullptr, out, &a, st) !=
           cudaSuccess)
@@ -1426,7 +1467,7 @@ int shared_launch(const kvq_cache_desc& d, int32_t S, int32_t Hq, const void* q,
     a.mtiles = (int)pl.prefix.mtiles; a.splits = pl.prefix.splits; a.shared_len = prefix_len;
     a.out = nullptr;
     a.part = pa;
-    if (launch_any(a, d.head_dim, (int)pl.prefix.ctas, st) != cudaSuccess) return KVQ_ERR_CUDA;
+    if (launch_any(a, d.head_dim, pl.prefix, st) != cudaSuccess) return KVQ_ERR_CUDA;
   }
   const int r = decode_scored_split_launch(d, S, Hq, q, seq_lens, max_seq_len, block_table,
                                            bt_stride, sm_scale, sc, prefix_len, k_codes, k_params,

@@ -300,3 +300,12 @@ def test_tensors_that_would_be_misread_are_refused():
                                  stream=st)     # its workspace and output live on that stream
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("G,n", [(4, 15), (4, 16), (4, 17), (5, 12), (5, 13), (8, 8), (8, 9), (1, 64)])
+@pytest.mark.parametrize("d", [128, 256])
+def test_rows_around_half_a_tile(G, n, d):
+    # up to 64 rows of a sequence the weights enter as two parts, on lanes of their own
+    b = Batch([700, n, 333], [n, n, 1], d=d, H=2, G=G, wide=20.0, seed=21)
+    b.check(b.run())
+    b.check(b.run(cap=20.0, window=150), cap=20.0, window=150)
