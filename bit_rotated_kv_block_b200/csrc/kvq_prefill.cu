@@ -108,10 +108,10 @@ struct PfCfg {
   // tensor-memory columns: S0, S1, O, then Q (d = 128) or P (d = 256)
   static constexpr int O_COL = 2 * KT;
   static constexpr int Q_COL = O_COL + D;
-  // weights P of tile j: over S j & 1 where both products have one shape (M 128, N 128:
-  // such products are executed in issue order, so the next S cannot overwrite
-  // a P still being read); in columns of their own at d = 256, whose products
-  // (N 64 and N 256) have no such order
+  // weights P of tile j: over S j & 1 at d = 128, where no other columns are
+  // left (the issuing warp lets O += P V complete before the next S is written
+  // there: products are only ordered among themselves where they share the
+  // accumulator); in columns of their own at d = 256
   static constexpr int P_COL = QT ? 0 : O_COL + D;
   static constexpr int P_STEP = QT ? KT : KT / 2;
   static_assert(O_COL + D + (QT ? D : KT) <= (int)kPfTmemCols, "tensor memory");
@@ -1117,8 +1117,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
       const uint64_t qd = umma_desc_kmajor(smem_u32(smem), 128, C::GRP);
       wait(&sh.qf, 0);
       // Round i: the products P V of tile i - 2, then Q K^T of tile i. With two
-      // stages they are issued back to back, their operands waited for before P,
-      // the last to come; with one the keys of tile i are widened while P V runs.
+      // stages the operands of both are waited for before P, the last to come;
+      // with one the keys of tile i are widened while P V runs. Where P lies
+      // under the S that Q K^T writes, P V completes first.
       for (int i = 0; i < ntile + 2; ++i) {
         const int j = i - 2;
         const int sk = NS == 2 ? (i & 1) : 0, sv = NS == 2 ? (j & 1) : 0;
@@ -1140,6 +1141,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
           }
         }
         __syncwarp();
+        if (C::P_COL == 0 && j >= 0 && i < ntile) {
+          wait(&sh.pv[j & 3], (j >> 2) & 1);
+          tc_fence_after();
+        }
         if (NS == 1 && i < ntile) {
           wait(&sh.kf[sk], i & 1);
           tc_fence_after();
