@@ -93,8 +93,10 @@ struct PfCfg {
   static constexpr int V_OFF = K_OFF + NS * K_B;
   // 4 slots of (scale, scale, offset, offset) per pair of keys
   static constexpr int PAR_OFF = V_OFF + NS * K_B;
-  static constexpr int BAD_OFF = PAR_OFF + 8 * KT * 4;  // 4 slots x 4 words
-  static constexpr int EX_OFF = BAD_OFF + 64;           // exchange: 2 slots x 4 quarters x 128 floats
+  // 4 slots of a bit per key (bad, or large) and a bit per large one
+  static constexpr int BAD_OFF = PAR_OFF + 8 * KT * 4;
+  static constexpr int BW = KT / 32;                    // words of a bit per key
+  static constexpr int EX_OFF = BAD_OFF + 4 * 8 * BW;   // exchange: 2 slots x 4 quarters x 128 floats
   static constexpr int ROW_OFF = EX_OFF + 2 * 4 * kPfRows * 4;  // PfRowState of 128 rows
   // Rows of the query as copied in, and of the output on its way out. The
   // pitch lets eight threads on the same channels of consecutive rows meet
@@ -223,6 +225,19 @@ __device__ __forceinline__ void pf_quarter_sync(int quarter) {
   asm volatile("bar.sync %0, %1;" ::"r"(1 + quarter), "n"(32 * kPfNW) : "memory");
   tc_fence_after();
 }
+// Barrier of a warpgroup: whether any of its threads holds p.
+__device__ __forceinline__ bool pf_group_any(int bar, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(bar), "r"((uint32_t)p)
+      : "memory");
+  return r != 0u;
+}
 // One butterfly stage between columns [a, a + 16) and [b, b + 16) of a row.
 __device__ __forceinline__ void pf_cross16(uint32_t scr, int a, int b) {
   uint32_t x[16], y[16];
@@ -329,13 +344,24 @@ __device__ __forceinline__ bool pf_range_ok(int q0, int n, int max_q, int T) {
   return q0 >= 0 && n >= 0 && n <= max_q && q0 <= T - n;
 }
 
-// The value of the largest code of a row with halved (scale, minimum): finite
-// if the minimum and so, linear in the code, every value of the row is.
-__device__ __forceinline__ __half pf_value_top(__half2 hp) {
-  return __hfma(__float2half(15.f), __low2half(hp), __high2half(hp));
-}
+// A value row is large if its (halved) largest dequantized value leaves the
+// binary16 range though its scale and minimum are finite: a constant row of
+// 20000 rotates to one channel of 226000. The values of a tile with such a
+// row (1048000 at most) are staged times 2^-kPfLarge, and the tile's weights
+// enter the product times 2^kPfLarge. (A factor per key, with its correction
+// of the weights' sum, cost 2 to 6% of every call's time.)
+constexpr int kPfLarge = 4;
 __device__ __forceinline__ __half2 pf_halved(uint32_t params) {
   return __hmul2(u32_as_h2(params), __float2half2_rn(0.5f));
+}
+enum PfValue { kPfPlain, kPfLargeRow, kPfNotFinite };
+__device__ __forceinline__ PfValue pf_value_kind(uint32_t params) {
+  const __half2 hp = pf_halved(params);
+  // (linear in the code: the ends are the minimum and the largest code's value)
+  const __half top = __hfma(__float2half(15.f), __low2half(hp), __high2half(hp));
+  if (__habs(top) <= __float2half(65504.f)) return kPfPlain;
+  const bool fin = (params & 0x7C00u) != 0x7C00u && (params & 0x7C000000u) != 0x7C000000u;
+  return fin ? kPfLargeRow : kPfNotFinite;
 }
 
 // Four bytes of codes (8 channels) as binary16 pairs in the operands' channel
@@ -364,7 +390,7 @@ __device__ __forceinline__ uint4 pf_codes_v(uint32_t x, __half2 s2, __half2 m2) 
 template <int D, bool OPT, bool PAIR>
 __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArgs a) {
   using C = PfCfg<D>;
-  constexpr int KT = C::KT, NS = C::NS;
+  constexpr int KT = C::KT, NS = C::NS, BW = C::BW;
   extern __shared__ __align__(1024) uint8_t smem[];
   PfShared& sh = *reinterpret_cast<PfShared*>(smem + C::BAR_OFF);
   PfRowState* const rst = reinterpret_cast<PfRowState*>(smem + C::ROW_OFF);
@@ -665,7 +691,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
       for (int nb = 0; nb < NB; ++nb)
         tmem_ld_frag<32>(tmem + lanes16 + (j & 1) * KT + 64 * nb, zr[nb]);
       const float4* ks = reinterpret_cast<const float4*>(smem + C::PAR_OFF) + (j & 3) * (KT / 2) + jl;
-      const uint32_t* const bads = reinterpret_cast<const uint32_t*>(smem + C::BAD_OFF + (j & 3) * 16);
+      const uint32_t* const bads = reinterpret_cast<const uint32_t*>(smem + C::BAD_OFF + (j & 3) * 8 * BW);
       const int base = (t0 + j) * KT;
       tmem_ld_wait();
       // z / rs = s'_j dot + m'_j qsum
@@ -776,10 +802,16 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
               zr[i >> 4][4 * ((i >> 1) & 7) + 2 * rr + (i & 1)] = 0xff800000u;
         }
       }
+      float up = 0.f;  // what the exponents of the tile's weights get on top
       if ((KT == 128 ? bads[0] | bads[1] | bads[2] | bads[3] : bads[0] | bads[1]) != 0u) {
+        if ((KT == 128 ? bads[4] | bads[5] | bads[6] | bads[7] : bads[2] | bads[3]) != 0u) {
+          up = (float)kPfLarge;
+          thr[0] -= kPfSlack;  // (no slack in this tile, so that they stay below 2^11)
+          thr[1] -= kPfSlack;
+        }
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-          const uint32_t bw = bads[i / 4] >> (8 * (i & 3) + 2 * jl);
+          const uint32_t bw = (bads[i / 4] & ~bads[BW + i / 4]) >> (8 * (i & 3) + 2 * jl);
 #pragma unroll
           for (int e = 0; e < 2; ++e)
             if ((bw >> e) & 1u)
@@ -842,7 +874,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
       for (int rr = 0; rr < 2; ++rr) {
         const float m1 = OPT ? 1.f : rs[rr];
         mu[rr] = pk(m1, m1);
-        of[rr] = pk(off[rr], off[rr]);
+        of[rr] = pk(off[rr] + up, off[rr] + up);
       }
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
@@ -871,7 +903,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
 #pragma unroll
       for (int rr = 0; rr < 2; ++rr) {
         const float2 f = upk(l2[rr]);
-        l[rr] += f.x + f.y;
+        l[rr] = fmaf(f.x + f.y, up != 0.f ? 1.f / (1 << kPfLarge) : 1.f, l[rr]);
+        if (up != 0.f && thr[rr] != -INFINITY) thr[rr] = kPfLift - off[rr] + kPfSlack;
       }
       tmem_st_wait();
       tc_fence_before();
@@ -1049,12 +1082,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
     // tile j (registers st): stage, then load tile j + 2 with the page pg2
     auto step = [&](int j, int st, int pg2) {
       const int sl = NS == 2 ? (j & 1) : 0;
-      if (j >= NS) {
-        // one warp polls for its warpgroup (polls of all eight took a tenth of
-        // the issue slots beside the softmax)
-        if ((warp & 3) == 0) wait(&empty[sl], NS == 2 ? ((j >> 1) - 1) & 1 : (j - 1) & 1);
-        asm volatile("bar.sync %0, 128;" ::"r"(5 + (int)isv) : "memory");
-      }
+      const PfValue kind = pf_value_kind(isv ? pr[st] : vr[st]);
+      // one warp polls for its warpgroup (polls of all eight took a tenth of
+      // the issue slots beside the softmax)
+      if (j >= NS && (warp & 3) == 0) wait(&empty[sl], NS == 2 ? ((j >> 1) - 1) & 1 : (j - 1) & 1);
+      const bool large = pf_group_any(5 + (int)isv, kind == kPfLargeRow);
       uint8_t* const dst = dst0 + sl * C::K_B;
       const uint32_t w4[16] = {
           cr[st][0].x, cr[st][0].y, cr[st][0].z, cr[st][0].w, cr[st][1].x, cr[st][1].y,
@@ -1064,7 +1096,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
         // halved: the largest dequantized value (15 s + m, s rounded up) may
         // exceed the binary16 range by its rounding
         __half2 hp = pf_halved(pr[st]);
-        if (!(__habs(pf_value_top(hp)) <= __float2half(65504.f))) hp = __float2half2_rn(0.f);
+        if (large) hp = __hmul2(hp, __float2half2_rn(1.f / (1 << kPfLarge)));
+        if (kind == kPfNotFinite) hp = __float2half2_rn(0.f);
         const __half2 s2 = __low2half2(hp), m2 = __high2half2(hp);
 #pragma unroll
         for (int w = 0; w < 16; ++w)
@@ -1073,14 +1106,17 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
         float* ks = reinterpret_cast<float*>(smem + C::PAR_OFF) + (j & 3) * 2 * KT +
                     (key >> 1) * 4 + (key & 1);
         const bool bd = (bad >> st) & 1u;
-        const uint32_t bm = __ballot_sync(0xffffffffu, bd);
+        const uint32_t lm = __ballot_sync(0xffffffffu, kind == kPfLargeRow);
+        const uint32_t bm = __ballot_sync(0xffffffffu, bd) | lm;
         if (part == 0) {
           const float2 sm = __half22float2(u32_as_h2(pr[st]));
-          // (0 x top: NaN unless it is finite)
-          ks[0] = fmaf(0.f, __half2float(pf_value_top(pf_halved(vr[st]))), sm.x * a.scale2);
+          ks[0] = kind == kPfNotFinite ? __int_as_float(0x7FC00000) : sm.x * a.scale2;
           ks[2] = fmaf(-64.f, sm.x, sm.y) * a.scale2;  // (the operand holds 64 + c)
-          if (lane == 0)
-            reinterpret_cast<uint32_t*>(smem + C::BAD_OFF + (j & 3) * 16)[key >> 5] = bm;
+          if (lane == 0) {
+            uint32_t* const bw = reinterpret_cast<uint32_t*>(smem + C::BAD_OFF + (j & 3) * 8 * BW);
+            bw[key >> 5] = bm;
+            bw[BW + (key >> 5)] = lm;
+          }
           if (bd && h == 0 && ((key & P1) == 0 || tok0 + j * KT == kv_lo)) raise_flag(a.err, KVQ_ERRF_PAGE);
         }
 #pragma unroll

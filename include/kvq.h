@@ -352,9 +352,12 @@ int kvq_decode_step(const kvq_cache_desc* desc, int32_t num_seqs, int32_t num_q_
  * (KVQ_ERRF_PAGE) are not seen.
  * Accuracy: weights p and the dequantized values enter the product as
  * binary16 (one rounding each), the query with about 22 bits and the key
- * codes exactly, all sums binary32; the result is rounded to binary16 once. A
- * token whose cached key or value is not finite affects the queries that see
- * it, and no others.
+ * codes exactly, all sums binary32; the result is rounded to binary16 once
+ * (to an infinity beyond its range). Dequantized values may exceed the
+ * binary16 range (a constant row rotates to one large channel); those of the
+ * 128 positions around such a token (64 at head_dim 256) are rounded to steps
+ * of 2^-19 at least. A token whose key or value has a scale or minimum that is
+ * not finite affects the queries that see it, and no others.
  */
 size_t kvq_prefill_workspace_bytes(const kvq_cache_desc* desc, int32_t num_seqs,
                                    int32_t num_q_heads, int32_t num_tokens, int32_t max_q_len,

@@ -2,11 +2,15 @@
 kernels' loops, number ranges and roundings are at their ends, against plain
 float64 attention over the same pages."""
 
+import math
+
 import pytest
 import torch
 
+from attn_plain import attention, half_tolerance, rows, seen_mask
 from bit_rotated_kv_block_b200 import kvq
 from test_gpu_prefill import Batch
+from test_gpu_scored import batch, share, shared
 
 pytestmark = pytest.mark.gpu
 
@@ -17,6 +21,38 @@ def refill(b, k, v):
     tp = torch.cat([torch.arange(n, dtype=torch.int32) for n in b.lens])
     kvq.quantize_append(b.cache, k.half().cuda().contiguous(), v.half().cuda().contiguous(),
                         ts.cuda(), tp.cuda(), b.table, b.kc, b.kp, b.vc, b.vp)
+
+
+def rows_of(b, s, q, pos, cap=0.0, window=0):
+    """Float64 results of one sequence's queries, with what their tolerances
+    take: (out, A, S, largest seen value of each row [n][1])."""
+    L = b.lens[s]
+    pages = b.table[s, :-(-L // b.P)].long()
+    k, v = rows(b.kc, b.kp, pages, b.d)[:L], rows(b.vc, b.vp, pages, b.d)[:L]
+    seen = seen_mask(L, pos, window)
+    ref, A, S = attention(q, k, v, pos, b.G, 1.0 / math.sqrt(b.d), b.R, cap, None, seen, b.rope)
+    top = torch.where(seen, v.abs().amax(-1).amax(-1), torch.zeros((), dtype=torch.float64,
+                                                                   device="cuda")).amax(1)
+    return ref, A, S, top[:, None]
+
+
+def check_prompt(b, out, cap=0.0, window=0):
+    """As Batch.check, with each row's tolerance from the values that it sees."""
+    for s, (L, n) in enumerate(zip(b.lens, b.qn)):
+        a = b.q_start[s]
+        ref, A, S, top = rows_of(b, s, b.q[a:a + n], torch.arange(L - n, L, device="cuda"), cap,
+                                 window)
+        off = (out[a:a + n].double() - ref).norm(dim=-1)
+        tol = half_tolerance(ref, A, S, L, top, cap)
+        assert bool((off <= tol).all()), (s, float((off / tol).max()), int(off.isnan().sum()))
+
+
+def check_shared(b, out, q, cap=0.0, window=0):
+    for s, L in enumerate(b.lens):
+        ref, A, S, top = rows_of(b, s, q[s:s + 1], torch.tensor([L - 1], device="cuda"), cap, window)
+        off = (out[s].double() - ref[0]).norm(dim=-1)
+        tol = half_tolerance(ref, A, S, L, top, cap)[0]
+        assert bool((off <= tol).all()), (s, float((off / tol).max()), int(off.isnan().sum()))
 
 
 @pytest.mark.parametrize("d,opt", [(128, dict()), (256, dict()), (128, dict(cap=40.0, window=3500)),
@@ -37,4 +73,44 @@ def test_long_unsplit_prompt_with_rising_scores(d, opt):
         kw["slopes"] = torch.tensor([2.0 ** (-4 - i) for i in range(4)], device="cuda")
     out = b.run(**kw)
     b.check(out, **kw)
+    assert int(b.err.item()) == 0
+
+
+def constant_tokens(b, value, at):
+    """Standard normal keys and values, with tokens whose values are one constant
+    in every channel (the Hadamard rotation gathers it in a channel per block).
+    A row's stored minimum is a binary16 number, so a negative constant goes no
+    lower than -65504 / sqrt(block); beyond it the cached row itself is infinite."""
+    g = torch.Generator().manual_seed(33)
+    T = sum(b.lens)
+    v = torch.randn((T, b.H, b.d), generator=g)
+    for i, t in enumerate(at):
+        v[t] = value if i % 2 == 0 else -min(value, 65000.0 / math.sqrt(b.d))
+    refill(b, torch.randn((T, b.H, b.d), generator=g), v)
+
+
+@pytest.mark.parametrize("value", [3000.0, 11700.0, 20000.0, 50000.0])
+@pytest.mark.parametrize("d,lens,qn", [(128, [300], [300]), (256, [200], [200]), (128, [2500], [40]),
+                                       (128, [700, 333], [8, 16]), (256, [1500], [3])], ids=str)
+def test_large_constant_values_are_finite(d, lens, qn, value):
+    # a constant row of c decodes to c sqrt(block) in one channel, far above the
+    # binary16 range for the larger ones, and is c again after the rotation back
+    b = Batch(lens, qn, d=d, H=2, G=4, block=d)
+    L, n = lens[0], qn[0]
+    constant_tokens(b, value, [L - n, L - n // 2, 5])
+    kw = dict(cap=30.0, window=100)
+    check_prompt(b, b.run())
+    check_prompt(b, b.run(**kw), **kw)
+    check_prompt(b, b.run(window=1), window=1)
+    assert int(b.err.item()) == 0
+
+
+@pytest.mark.parametrize("value", [11700.0, 20000.0, 50000.0])
+@pytest.mark.parametrize("d", [128, 256])
+def test_large_constant_values_in_a_shared_prefix(d, value):
+    b, q = batch([310, 420, 555], d=d, block=d, seed=34)
+    constant_tokens(b, value, [7, 200, 299])
+    share(b, 300)
+    for kw in (dict(), dict(cap=30.0, window=300)):
+        check_shared(b, shared(b, q, 300, **kw), q, **kw)
     assert int(b.err.item()) == 0
