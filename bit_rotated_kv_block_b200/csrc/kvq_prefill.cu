@@ -344,19 +344,15 @@ __device__ __forceinline__ bool pf_range_ok(int q0, int n, int max_q, int T) {
   return q0 >= 0 && n >= 0 && n <= max_q && q0 <= T - n;
 }
 
-// A value row is large if its (halved) largest dequantized value leaves the
-// binary16 range though its scale and minimum are finite: a constant row of
+// A value row is large if its largest dequantized value leaves the binary16 range though its scale and minimum are finite: a constant row of
 // 20000 rotates to one channel of 226000. The values of a tile with such a
 // row (1048000 at most) are staged times 2^-kPfLarge, and the tile's weights
 // enter the product times 2^kPfLarge. (A factor per key, with its correction
 // of the weights' sum, cost 2 to 6% of every call's time.)
-constexpr int kPfLarge = 4;
-__device__ __forceinline__ __half2 pf_halved(uint32_t params) {
-  return __hmul2(u32_as_h2(params), __float2half2_rn(0.5f));
-}
+constexpr int kPfLarge = 5;
 enum PfValue { kPfPlain, kPfLargeRow, kPfNotFinite };
 __device__ __forceinline__ PfValue pf_value_kind(uint32_t params) {
-  const __half2 hp = pf_halved(params);
+  const __half2 hp = u32_as_h2(params);
   // (linear in the code: the ends are the minimum and the largest code's value)
   const __half top = __hfma(__float2half(15.f), __low2half(hp), __high2half(hp));
   if (__habs(top) <= __float2half(65504.f)) return kPfPlain;
@@ -806,7 +802,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
       if ((KT == 128 ? bads[0] | bads[1] | bads[2] | bads[3] : bads[0] | bads[1]) != 0u) {
         if ((KT == 128 ? bads[4] | bads[5] | bads[6] | bads[7] : bads[2] | bads[3]) != 0u) {
           up = (float)kPfLarge;
-          thr[0] -= kPfSlack;  // (no slack in this tile, so that they stay below 2^11)
+          thr[0] -= kPfSlack;  // (no slack in this tile, so that they stay below 2^12)
           thr[1] -= kPfSlack;
         }
 #pragma unroll
@@ -938,7 +934,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
                                  __shfl_down_sync(0xffffffffu, __uint_as_float(o[i]), 16));
       }
     };
-    // ---- the thread's channels of its row's result (V entered halved)
+    // ---- the thread's channels of its row's result
     if (a.part != nullptr) {
       float* dst = a.part + (R.row * a.splits + split) * (D + 4);
       const bool some = ntile > 0 && Mr != -INFINITY;
@@ -955,10 +951,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
 #pragma unroll
               for (int q = 0; q < 2; ++q) {
                 float4 f;
-                f.x = 2.f * __uint_as_float(o[8 * k + 0 + q]);
-                f.y = 2.f * __uint_as_float(o[8 * k + 2 + q]);
-                f.z = 2.f * __uint_as_float(o[8 * k + 4 + q]);
-                f.w = 2.f * __uint_as_float(o[8 * k + 6 + q]);
+                f.x = __uint_as_float(o[8 * k + 0 + q]);
+                f.y = __uint_as_float(o[8 * k + 2 + q]);
+                f.z = __uint_as_float(o[8 * k + 4 + q]);
+                f.w = __uint_as_float(o[8 * k + 6 + q]);
                 *reinterpret_cast<float4*>(dst + c + 8 * k + 4 * q) = f;
               }
           }
@@ -968,7 +964,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
       if (R.valid && wg == 0)
         *reinterpret_cast<float2*>(dst + D) = make_float2(some ? Mr : -INFINITY, lr);
     } else {
-      const float inv = lr > 0.f ? 2.f / lr : lr;  // (NaN stays)
+      const float inv = lr > 0.f ? 1.f / lr : lr;  // (NaN stays)
       const bool zero = Mr == -INFINITY;
       if (ntile > 0) {
         // normalised, back in channel order, then R^-1
@@ -1093,9 +1089,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
           cr[st][1].z, cr[st][1].w, cr[st][2].x, cr[st][2].y, cr[st][2].z, cr[st][2].w,
           cr[st][3].x, cr[st][3].y, cr[st][3].z, cr[st][3].w};
       if (isv) {
-        // halved: the largest dequantized value (15 s + m, s rounded up) may
-        // exceed the binary16 range by its rounding
-        __half2 hp = pf_halved(pr[st]);
+        __half2 hp = u32_as_h2(pr[st]);
         if (large) hp = __hmul2(hp, __float2half2_rn(1.f / (1 << kPfLarge)));
         if (kind == kPfNotFinite) hp = __float2half2_rn(0.f);
         const __half2 s2 = __low2half2(hp), m2 = __high2half2(hp);

@@ -114,3 +114,28 @@ def test_large_constant_values_in_a_shared_prefix(d, value):
     for kw in (dict(), dict(cap=30.0, window=300)):
         check_shared(b, shared(b, q, 300, **kw), q, **kw)
     assert int(b.err.item()) == 0
+
+
+@pytest.mark.parametrize("size", [1e-3, 3e-4, 1e-4, 3e-5])
+@pytest.mark.parametrize("d,lens,qn", [(128, [300], [300]), (256, [200], [200]), (128, [700, 333], [8, 16])],
+                         ids=str)
+def test_small_values_keep_their_bits(d, lens, qn, size):
+    # value scales of a few binary16 subnormal steps; one-key windows give the
+    # dequantized rows themselves
+    b = Batch(lens, qn, d=d, H=2, G=4, block=64)
+    g = torch.Generator().manual_seed(35)
+    T = sum(lens)
+    refill(b, torch.randn((T, 2, d), generator=g), size * torch.randn((T, 2, d), generator=g))
+    for kw in (dict(window=1), dict(), dict(cap=20.0, window=50)):
+        check_prompt(b, b.run(**kw), **kw)
+
+
+@pytest.mark.parametrize("size", [1e-3, 1e-4, 3e-5])
+def test_small_values_in_a_shared_prefix(size):
+    b, q = batch([301, 302, 303], seed=36)
+    g = torch.Generator().manual_seed(37)
+    T = sum(b.lens)
+    v = size * torch.randn((T, b.H, b.d), generator=g)
+    refill(b, torch.randn((T, b.H, b.d), generator=g), v)
+    share(b, 300)
+    check_shared(b, shared(b, q, 300), q)
