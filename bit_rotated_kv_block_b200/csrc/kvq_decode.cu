@@ -628,7 +628,35 @@ __global__ void __launch_bounds__(kDecWarps * kWarp, D == 256 ? 2 : 3)
     }
     const int tok0 = (pg_lo + gi * C::PG) * P;  // first token of the group
     // groups whose every token is cached skip all per-token masking
-    const bool full = all_ok && tok0 + C::PG * P <= L && (!SC || tok0 >= lo_tok);
+    bool full = all_ok && tok0 + C::PG * P <= L && (!SC || tok0 >= lo_tok);
+    // SC: weights p s enter the product as binary16 pairs. The largest value
+    // scale of the group's seen tokens has to leave them in range: above 2^7
+    // no p may exceed 1 (no slack), below 2^-4 they get a power of two, which
+    // comes off again when the stage is added. Either goes through the masked
+    // form. (The check takes 1.5% of a full batch, 40.3 -> 40.9 us; held back
+    // until the scores are formed it took 2.7%.)
+    float slack = kMaxSlack, up = 1.f, down = 1.f;
+    if (SC) {
+      uint32_t top = 0u;
+#pragma unroll
+      for (int k = 0; k < C::TPG / 2; ++k) {
+        const int t = 32 * k + lane;
+        const uint32_t sw = *reinterpret_cast<const uint32_t*>(st + (t / P) * C::PAGE_B + 2 * C::CODE_B +
+                                                               P * 4 + (t % P) * 4) & 0x7FFFu;
+        if (full || (tok0 + t < L && tok0 + t >= lo_tok)) top = max(top, sw);
+      }
+      top = __reduce_max_sync(0xffffffffu, top);
+      if (top - 0x2C00u > 0x2C00u && top != 0u) {  // binary16 patterns of 2^-4 and 2^7
+        full = false;
+        if (top > 0x2C00u) {
+          slack = 0.f;
+        } else {
+          const int e = (__float_as_int(__half2float(__ushort_as_half((unsigned short)top))) >> 23) - 127;
+          up = __int_as_float((127 + 6 - e) << 23);
+          down = __int_as_float((127 - 6 + e) << 23);
+        }
+      }
+    }
 
     auto body = [&](auto masked_tag) {
       constexpr bool MASKED = decltype(masked_tag)::value;
@@ -718,7 +746,7 @@ __global__ void __launch_bounds__(kDecWarps * kWarp, D == 256 ? 2 : 3)
       for (int tt = 0; tt < C::TPG; ++tt)
 #pragma unroll
         for (int e = 0; e < NE; ++e) mloc = fmaxf(mloc, z[tt][e]);
-      if (__any_sync(0xffffffffu, mloc > M + kMaxSlack)) {
+      if (__any_sync(0xffffffffu, mloc > M + (SC && MASKED ? slack : kMaxSlack))) {
         mloc = fmaxf(mloc, __shfl_xor_sync(0xffffffffu, mloc, 1));
         mloc = fmaxf(mloc, __shfl_xor_sync(0xffffffffu, mloc, 2));
         if (GP == 4) mloc = fmaxf(mloc, __shfl_xor_sync(0xffffffffu, mloc, 16));
@@ -772,6 +800,7 @@ __global__ void __launch_bounds__(kDecWarps * kWarp, D == 256 ? 2 : 3)
           Lp += p;
           Op = live ? fmaf(p, fmaf(8.f, sm.x, sm.y), Op) : Op;  // p (m_v + 8 s_v)
           wv[e] = live ? p * sm.x : 0.f;
+          if (SC && MASKED) wv[e] *= up;
         }
         // weights p * s as binary16 hi + lo pairs: hi = RN16(w), lo = RN16(w - hi)
         uint32_t bh[2], bl[2];
@@ -862,7 +891,8 @@ __global__ void __launch_bounds__(kDecWarps * kWarp, D == 256 ? 2 : 3)
               mma16816_z(u4, av, bh[0], bh[1]);
               if (GP == 8) mma16816(u4, av, bl[0], bl[1]);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) acc[mt][e] += u4[e];
+              for (int e = 0; e < 4; ++e)
+                acc[mt][e] = SC && MASKED ? fmaf(u4[e], down, acc[mt][e]) : acc[mt][e] + u4[e];
             }
           }
         }
@@ -871,7 +901,8 @@ __global__ void __launch_bounds__(kDecWarps * kWarp, D == 256 ? 2 : 3)
 #pragma unroll
         for (int mt = 0; mt < C::NMT; ++mt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[mt][e] += t4[mt][e];
+          for (int e = 0; e < 4; ++e)
+            acc[mt][e] = SC && MASKED ? fmaf(t4[mt][e], down, acc[mt][e]) : acc[mt][e] + t4[mt][e];
       }
     };
     if (full)

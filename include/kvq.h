@@ -267,7 +267,10 @@ size_t kvq_decode_workspace_bytes(const kvq_cache_desc* desc, int32_t num_seqs,
  * z_j = sm_scale * qhat . khat_j; p = softmax(z); out = R^-1 sum_j p_j vhat_j,
  * with khat_j, vhat_j the dequantized rows. Results match a double-precision
  * evaluation of that definition to about 1e-4 absolute for unit-scale data
- * (the contractions run on tensor cores with split binary16 operands).
+ * (the contractions run on tensor cores with split binary16 operands). The
+ * operands hold p times a value scale: from scales of 2^8 on they can leave
+ * the binary16 range (NaN), below 2^-10 they lose bits;
+ * kvq_paged_decode_attn_scored without options follows the scales instead.
  */
 int kvq_paged_decode_attn(const kvq_cache_desc* desc, int32_t num_seqs, int32_t num_q_heads,
                           const void* q, const int32_t* seq_lens, int32_t max_seq_len,
@@ -378,8 +381,10 @@ int kvq_paged_prefill_attn(const kvq_cache_desc* desc, int32_t num_seqs, int32_t
  * sequence, prefix_lens must be NULL. Pages that lie wholly before the
  * window or the document are not read (their table entries may be stale).
  * INT4 pages (KVQ_FMT_INT4; others return KVQ_ERR_UNSUPPORTED); all other
- * arguments, the workspace (kvq_decode_workspace_bytes), the accuracy, the
- * return codes and the flags as for kvq_paged_decode_attn.
+ * arguments, the workspace (kvq_decode_workspace_bytes), the return codes
+ * and the flags as for kvq_paged_decode_attn. Accuracy as there, relative to
+ * sum_j p_j |vhat_j| for value scales of any size (tokens of very different
+ * scales within 64 positions: to 2^-25 of the largest, in weight).
  */
 int kvq_paged_decode_attn_scored(const kvq_cache_desc* desc, int32_t num_seqs,
                                  int32_t num_q_heads, const void* q, const int32_t* seq_lens,

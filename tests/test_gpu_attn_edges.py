@@ -7,10 +7,10 @@ import math
 import pytest
 import torch
 
-from attn_plain import attention, half_tolerance, rows, seen_mask
+from attn_plain import attention, float_tolerance, half_tolerance, rows, seen_mask
 from bit_rotated_kv_block_b200 import kvq
 from test_gpu_prefill import Batch
-from test_gpu_scored import batch, share, shared
+from test_gpu_scored import batch, scored, share, shared
 
 pytestmark = pytest.mark.gpu
 
@@ -139,3 +139,65 @@ def test_small_values_in_a_shared_prefix(size):
     refill(b, torch.randn((T, b.H, b.d), generator=g), v)
     share(b, 300)
     check_shared(b, shared(b, q, 300), q)
+
+
+def lagging_batch(d, G, P, values, seed):
+    """Sequences of 200 tokens of which one warp attends all (more pairs than
+    resident warps), and queries whose score rises by about six bits at two
+    tokens: less than moves the running reference. ``values(g, T, H)``: the
+    value rows of a sequence, of which rows 100 and 130 are those tokens'."""
+    b, q = batch([200] * 3 + [1] * 117, d=d, H=16, G=G, P=P, block=d, seed=seed)
+    g = torch.Generator().manual_seed(seed)
+    u = torch.randn((1, 1, d), generator=g)
+    T = sum(b.lens)
+    k = 0.02 * torch.randn((T, 16, d), generator=g)
+    v = torch.randn((T, 16, d), generator=g)
+    for s in range(3):
+        k[200 * s + 100] = k[200 * s + 130] = 4.0 / math.sqrt(d) * u[0]
+        v[200 * s:200 * s + 200] = values(g, 200, 16)
+    refill(b, k, v)
+    return b, (u + 0.05 * torch.randn(q.shape, generator=g)).half().cuda()
+
+
+def check_scored(b, out, q, count, cap=0.0, window=0):
+    for s in range(count):
+        L = b.lens[s]
+        ref, A, S, _ = rows_of(b, s, q[s:s + 1], torch.tensor([L - 1], device="cuda"), cap, window)
+        off = (out[s].double() - ref[0]).norm(dim=-1)
+        tol = float_tolerance(A, S, L, cap)[0]
+        assert bool((off <= tol).all()), (s, float((off / tol).max()), int(off.isnan().sum()))
+
+
+@pytest.mark.parametrize("size", [3e-5, 1e-4, 1e-3, 1e-2, 0.1, 30.0, 2000.0, 20000.0, 50000.0])
+@pytest.mark.parametrize("d,G,P", [(128, 4, 16), (128, 8, 32), (128, 3, 64), (256, 4, 16), (256, 2, 64)])
+def test_scored_over_value_sizes(d, G, P, size):
+    def values(g, T, H):
+        if size <= 30.0:
+            return size * torch.randn((T, H, d), generator=g)
+        v = torch.randn((T, H, d), generator=g)
+        v[100], v[130] = size, -min(size, 65000.0 / math.sqrt(d))  # (binary16 minimum)
+        return v
+    b, q = lagging_batch(d, G, P, values, 41)
+    for kw in (dict(), dict(cap=30.0, window=150)):
+        check_scored(b, scored(b, q, **kw), q, 3, **kw)
+    assert int(b.err.item()) == 0
+
+
+@pytest.mark.parametrize("size", [1e-4, 20000.0])
+@pytest.mark.parametrize("d", [128, 256])
+def test_own_part_behind_a_prefix_over_value_sizes(d, size):
+    # (a prefix of one token: nearly every position is the own part's)
+    def values(g, T, H):
+        v = min(size, 1.0) * torch.randn((T, H, d), generator=g)
+        if size > 1.0:
+            v[100] = v[130] = size
+        return v
+    b, q = lagging_batch(d, 4, 16, values, 42)
+    share(b, 1)
+    check_shared_some(b, shared(b, q, 1), q, 3)
+
+
+def check_shared_some(b, out, q, count):
+    lens, b.lens = b.lens, b.lens[:count]
+    check_shared(b, out, q)
+    b.lens = lens
