@@ -1228,8 +1228,7 @@ int decode_scored_split_launch(const kvq_cache_desc& d, int32_t S, int32_t Hq, c
   a.skip = skip;
   a.beside = beside;
   if (sc != nullptr) {
-    a.capk = sc->softcap > 0.f ? 2.f / sc->softcap : 0.f;
-    a.cap2 = (float)((double)sc->softcap * 1.4426950408889634074);
+    score_cap(sc, a.capk, a.cap2);
     a.window = sc->window;
     a.alibi = sc->alibi;
     a.first_pos = sc->first_pos;

@@ -92,6 +92,15 @@ int decode_scored_launch(const kvq_cache_desc& d, int32_t S, int32_t Hq, const v
                          const uint8_t* v_codes, const void* v_params, float* out,
                          void* workspace, size_t workspace_bytes, int32_t* err, cudaStream_t st);
 
+// The cap of the options in base-2 units: capk = 2 / cap and cap2 = cap log2(e),
+// both 0 for none. From 1e30 on a cap is none: it changes no score by half a
+// rounding, while cap2 nears the end of the binary32 range.
+inline void score_cap(const kvq_score_desc* sc, float& capk, float& cap2) {
+  const bool on = sc != nullptr && sc->softcap > 0.f && sc->softcap < 1e30f;
+  capk = on ? 2.f / sc->softcap : 0.f;
+  cap2 = on ? (float)((double)sc->softcap * 1.4426950408889634074) : 0.f;
+}
+
 // The merge kernel over split partial results [S][Hq][splits][d + 4] (the
 // running sums, then the base-2 maximum and total weight), rotated back.
 // Query heads of the first `nhi` (sequence, KV head) pairs combine `splits`

@@ -1397,8 +1397,7 @@ static void fill_args(PrefillArgs& a, const kvq_cache_desc& d, int32_t S, int32_
   a.rot_kind = d.rot_kind; a.lgb = log2i(d.rot_block);
   a.hscale = hadamard_scale(a.lgb);
   a.scale2 = (float)((double)sm_scale * 1.4426950408889634074);
-  a.capk = sc && sc->softcap > 0.f ? 2.f / sc->softcap : 0.f;
-  a.cap2 = sc ? (float)((double)sc->softcap * 1.4426950408889634074) : 0.f;
+  score_cap(sc, a.capk, a.cap2);
   a.window = sc ? sc->window : 0;
   a.alibi = sc ? sc->alibi : nullptr;
   a.first_pos = sc ? sc->first_pos : nullptr;

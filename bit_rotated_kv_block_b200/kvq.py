@@ -220,6 +220,8 @@ class Score:
         self._alibi, self._first_pos, self._prefix_lens = alibi, first_pos, prefix_lens
         self.desc = ScoreDesc(softcap, window, *(None if t is None else t.data_ptr()
                                                  for t in (alibi, first_pos, prefix_lens)))
+        if softcap != 0.0 and self.desc.softcap == 0.0:
+            raise ValueError("softcap must be 0 or a float32 number of at least 1e-6")
 
     alibi = property(lambda self: self._alibi)
     first_pos = property(lambda self: self._first_pos)

@@ -184,7 +184,8 @@ typedef struct {
  * and position j is seen if j < L, (j <= p or j < prefix_lens[s]),
  * j > p - window (window > 0) and j >= first_pos[t]; a query that sees
  * nothing has the output 0.
- *  softcap      bound of the scores' magnitude, finite: 0 (none) or >= 1e-6.
+ *  softcap      bound of the scores' magnitude, finite: 0 (none) or >= 1e-6;
+ *               1e30 and more act as none.
  *  window       positions a query sees, its own included, >= 0; 0: all.
  *  alibi        device float [num_q_heads], finite slopes, or NULL.
  *  first_pos    device int32, one per query token, or NULL: the start of the

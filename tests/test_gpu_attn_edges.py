@@ -201,3 +201,18 @@ def check_shared_some(b, out, q, count):
     lens, b.lens = b.lens, b.lens[:count]
     check_shared(b, out, q)
     b.lens = lens
+
+
+@pytest.mark.parametrize("cap", [1e25, 1e30, 2e38, 3.4028234e38])
+@pytest.mark.parametrize("d", [128, 256])
+def test_a_huge_cap_is_none(d, cap):
+    b, q = batch([700, 333], d=d, seed=51)
+    share(b, 300)
+    for call, chk in ((scored, lambda o: check_scored(b, o, q, 2)),
+                      (lambda *a, **k: shared(*a[:2], 300, **k), lambda o: check_shared(b, o, q))):
+        chk(call(b, q, cap=cap))
+    p = Batch([300, 90], [300, 20], d=d, seed=52)
+    p.check(p.run(cap=cap))
+    if cap >= 1e30:
+        assert torch.equal(p.run(cap=cap), p.run())
+        assert torch.equal(scored(b, q, cap=cap), scored(b, q))
