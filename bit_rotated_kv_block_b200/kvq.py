@@ -110,34 +110,72 @@ def _ptr(t):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream):
+def _stream(stream, dev=None):
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(torch.cuda.current_device() if dev is None else dev)
         stream = torch.cuda.current_stream()
     return stream.cuda_stream
 
 
 def _ints(t, n, name, dev):
-    if t.dtype is not torch.int32 or t.numel() < n or not t.is_contiguous() or t.get_device() != dev:
+    if t.dtype is not _INT or t.numel() < n or not t.is_contiguous() or t.get_device() != dev:
         raise ValueError(f"{name} must be a contiguous int32 tensor of {n} entries on cuda:{dev}")
+
+
+_U8, _INT, _HALF = torch.uint8, torch.int32, torch.float16
+
+
+def _pool(t, shape, dtype, name):
+    """One pool of a cache: contiguous, of the cache's shape (or that with more
+    pages, or the same bytes in fewer or more dimensions)."""
+    if t.dtype is dtype and t.is_contiguous():
+        have = t.shape
+        if have == shape or (len(have) == len(shape) and have[1:] == shape[1:]
+                             and have[0] > shape[0]) \
+                or (len(have) != len(shape) and t.numel() == math.prod(shape)):
+            return
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)}")
+
+
+def _memory(cache, kc, kp, vc, vp, workspace, err):
+    """Checks of what the kernels address by the cache's geometry alone: pools of
+    another type, layout or size would be misread or read past their end."""
+    codes, params, cs, ps, cn, pn = cache.pool_layout
+    # (the strides and size of a contiguous tensor of the shape: half the host
+    # time of comparing shapes)
+    if not (kc.stride() == cs and vc.stride() == cs and kp.stride() == ps and vp.stride() == ps
+            and kc.nbytes == cn and vc.nbytes == cn and kp.nbytes == pn and vp.nbytes == pn
+            and kc.dtype is vc.dtype is _U8 and kp.dtype is vp.dtype is _INT):
+        _pool(kc, codes, torch.uint8, "k_codes")
+        _pool(vc, codes, torch.uint8, "v_codes")
+        _pool(kp, params, torch.int32, "k_params")
+        _pool(vp, params, torch.int32, "v_params")
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    if err is not None and (err.dtype is not _INT or err.numel() < 1):
+        raise ValueError("err must be an int32 tensor")
 
 
 def _fit(cache, q, seqs, seq_lens, block_table, kc, kp, vc, vp, out, out_dtype, workspace, err):
     """Checks of the attention entry points with options: every tensor on the
     current device (the library launches there; call inside
     ``torch.cuda.device(...)`` for another), queries and outputs of the
-    geometry, index tensors int32 and contiguous. What the kernels would
-    misread is refused here. Returns q's shape and the device."""
+    geometry, index tensors int32 and contiguous, pools of the cache's shape.
+    ``seqs`` None: one per query row. Returns q's shape and the device."""
     dev = torch.cuda.current_device()
     shape = q.shape
-    if q.dtype is not torch.float16 or len(shape) != 3 or shape[2] != cache.d:
+    _memory(cache, kc, kp, vc, vp, workspace, err)
+    if q.dtype is not _HALF or len(shape) != 3 or shape[2] != cache.d:
         raise ValueError(f"q must be float16 [rows][Hq][{cache.d}]")
+    if seqs is None:
+        seqs = shape[0]
     if out is not None and (out.dtype is not out_dtype or out.shape != shape
                             or not out.is_contiguous() or out.get_device() != dev):
         raise ValueError(f"out must be a contiguous {out_dtype} tensor of q's shape on cuda:{dev}")
     _ints(seq_lens, seqs, "seq_lens", dev)
-    if block_table.dim() != 2 or block_table.shape[0] < seqs:
+    rows = block_table.shape
+    if len(rows) != 2 or rows[0] < seqs:
         raise ValueError("block_table must have a row per sequence")
     _ints(block_table, 0, "block_table", dev)
     if not (q.get_device() == kc.get_device() == kp.get_device() == vc.get_device()
@@ -175,6 +213,11 @@ class Cache:
             self.levels = torch.as_tensor(levels, dtype=torch.float32).contiguous().to(device)
         self.d, self.H, self.P, self.NP = head_dim, num_kv_heads, page_size, num_pages
         self.rot_kind, self.rot_block = rot_kind, rot_block
+        # shapes, strides and bytes of the code pools and of the parameter pools
+        r = self.code_row_bytes()
+        H, P = num_kv_heads, page_size
+        self.pool_layout = ((num_pages, H, P, r), (num_pages, H, P), (H * P * r, P * r, r, 1),
+                            (H * P, P, 1), num_pages * H * P * r, 4 * num_pages * H * P)
         self.quat = None  # the rotation's table: quaternions, or signs
         if rot_kind in (ROT_QUAT, ROT_QUAT_FAST, ROT_HADAMARD_SIGNED, ROT_QUAT_MAT):
             self.quat = torch.as_tensor(quat, dtype=torch.float32).contiguous().to(device)
@@ -220,6 +263,8 @@ class Score:
         self._alibi, self._first_pos, self._prefix_lens = alibi, first_pos, prefix_lens
         self.desc = ScoreDesc(softcap, window, *(None if t is None else t.data_ptr()
                                                  for t in (alibi, first_pos, prefix_lens)))
+        self.held = tuple((t, n) for t, n in ((alibi, "alibi"), (first_pos, "first_pos"),
+                                              (prefix_lens, "prefix_lens")) if t is not None)
         if softcap != 0.0 and self.desc.softcap == 0.0:
             raise ValueError("softcap must be 0 or a float32 number of at least 1e-6")
 
@@ -228,15 +273,17 @@ class Score:
     prefix_lens = property(lambda self: self._prefix_lens)
 
 
-def _score(score, q, seqs):
+def _score(score, q, seqs, shape=None):
     """The options' descriptor for queries ``q`` [rows][Hq][d] of ``seqs``
     sequences; their tensors have to fit them."""
     if score is None:
         return None
-    for t, n, name in ((score.alibi, q.shape[1], "alibi"), (score.first_pos, q.shape[0], "first_pos"),
-                       (score.prefix_lens, seqs, "prefix_lens")):
-        if t is not None and (t.numel() != n or t.device != q.device):
-            raise ValueError(f"{name} must hold {n} entries on {q.device}")
+    if score.held:
+        rows, heads, _ = shape or q.shape
+        for t, name in score.held:
+            n = heads if name == "alibi" else rows if name == "first_pos" else seqs
+            if t.numel() != n or t.device != q.device:
+                raise ValueError(f"{name} must hold {n} entries on {q.device}")
     return ctypes.byref(score.desc)
 
 
@@ -326,8 +373,9 @@ def paged_prefill_attn(cache, q, q_start, max_q_len, seq_lens, max_seq_len, bloc
     [q_start[s], q_start[s + 1]), its last positions; returns float16
     [T][Hq][d]. ``score``: a ``Score`` (None: plain causal)."""
     S = seq_lens.numel()
-    (T, Hq, d), dev = _fit(cache, q, S, seq_lens, block_table, k_codes, k_params, v_codes, v_params,
-                           out, torch.float16, workspace, err)
+    shape, dev = _fit(cache, q, S, seq_lens, block_table, k_codes, k_params, v_codes, v_params, out,
+                      torch.float16, workspace, err)
+    T, Hq, d = shape
     _ints(q_start, S + 1, "q_start", dev)
     if q.stride(2) != 1 or (Hq > 1 and q.stride(1) != d):
         raise ValueError("q rows of a token must be contiguous")
@@ -341,9 +389,9 @@ def paged_prefill_attn(cache, q, q_start, max_q_len, seq_lens, max_seq_len, bloc
     st = lib().kvq_paged_prefill_attn(
         ctypes.byref(cache.desc), S, Hq, T, q.data_ptr(), q.stride(0) if T > 1 else Hq * d,
         q_start.data_ptr(), int(max_q_len), seq_lens.data_ptr(), int(max_seq_len),
-        block_table.data_ptr(), int(block_table.shape[1]), float(sm_scale), _score(score, q, S),
+        block_table.data_ptr(), int(block_table.shape[1]), float(sm_scale), _score(score, q, S, shape),
         k_codes.data_ptr(), k_params.data_ptr(), v_codes.data_ptr(), v_params.data_ptr(),
-        out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _ptr(err), _stream(stream))
+        out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _ptr(err), _stream(stream, dev))
     _check("kvq_paged_prefill_attn", st)
     return out
 
@@ -353,8 +401,9 @@ def paged_decode_attn_scored(cache, q, seq_lens, max_seq_len, block_table, k_cod
                              sm_scale=None, err=None, stream=None):
     """``paged_decode_attn`` with scoring options (a ``Score``; its first_pos
     has one entry per sequence); same workspace."""
-    (S, Hq, d), _ = _fit(cache, q, q.shape[0], seq_lens, block_table, k_codes, k_params, v_codes,
-                         v_params, out, torch.float32, workspace, err)
+    shape, dev = _fit(cache, q, None, seq_lens, block_table, k_codes, k_params, v_codes, v_params,
+                      out, torch.float32, workspace, err)
+    S, Hq, d = shape
     if not q.is_contiguous():
         raise ValueError("q must be contiguous")
     if sm_scale is None:
@@ -366,9 +415,9 @@ def paged_decode_attn_scored(cache, q, seq_lens, max_seq_len, block_table, k_cod
         workspace = _new(max(need, 16), torch.uint8, q, stream)
     st = lib().kvq_paged_decode_attn_scored(
         ctypes.byref(cache.desc), S, Hq, q.data_ptr(), seq_lens.data_ptr(), int(max_seq_len),
-        block_table.data_ptr(), int(block_table.shape[1]), float(sm_scale), _score(score, q, S),
+        block_table.data_ptr(), int(block_table.shape[1]), float(sm_scale), _score(score, q, S, shape),
         k_codes.data_ptr(), k_params.data_ptr(), v_codes.data_ptr(), v_params.data_ptr(),
-        out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _ptr(err), _stream(stream))
+        out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _ptr(err), _stream(stream, dev))
     _check("kvq_paged_decode_attn_scored", st)
     return out
 
@@ -385,8 +434,9 @@ def shared_prefix_decode_attn(cache, q, prefix_len, seq_lens, max_seq_len, block
     ``prefix_len`` tokens (pages taken from row 0 of the table, read once for
     the batch); ``seq_lens`` are whole lengths. q: float16 CUDA [S][Hq][d];
     returns float16 [S][Hq][d]."""
-    (S, Hq, d), _ = _fit(cache, q, q.shape[0], seq_lens, block_table, k_codes, k_params, v_codes,
-                         v_params, out, torch.float16, workspace, err)
+    shape, dev = _fit(cache, q, None, seq_lens, block_table, k_codes, k_params, v_codes, v_params,
+                      out, torch.float16, workspace, err)
+    S, Hq, d = shape
     if not q.is_contiguous():
         raise ValueError("q must be contiguous")
     if sm_scale is None:
@@ -399,9 +449,9 @@ def shared_prefix_decode_attn(cache, q, prefix_len, seq_lens, max_seq_len, block
     st = lib().kvq_shared_prefix_decode_attn(
         ctypes.byref(cache.desc), S, Hq, q.data_ptr(), int(prefix_len), seq_lens.data_ptr(),
         int(max_seq_len), block_table.data_ptr(), int(block_table.shape[1]), float(sm_scale),
-        _score(score, q, S), k_codes.data_ptr(), k_params.data_ptr(), v_codes.data_ptr(),
+        _score(score, q, S, shape), k_codes.data_ptr(), k_params.data_ptr(), v_codes.data_ptr(),
         v_params.data_ptr(), out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _ptr(err),
-        _stream(stream))
+        _stream(stream, dev))
     _check("kvq_shared_prefix_decode_attn", st)
     return out
 

@@ -2,6 +2,7 @@
 binding (no GPU)."""
 
 import pytest
+import torch
 
 from bit_rotated_kv_block_b200 import kvq
 
@@ -12,3 +13,51 @@ def test_a_softcap_that_float32_cannot_hold_is_refused():
             kvq.Score(softcap=cap)       # it would act as no cap
     assert kvq.Score(softcap=0.0).desc.softcap == 0.0
     assert kvq.Score(softcap=50.0).desc.softcap == 50.0
+
+
+class Pools:
+    """A small cache's geometry on the CPU, with pools that fit it."""
+
+    def __init__(self):
+        self.cache = kvq.Cache(128, 2, 16, 6, kvq.ROT_HADAMARD, 64, device="cpu")
+        self.kc, self.kp = self.cache.new_pools(device="cpu", fill=0)
+        self.vc, self.vp = self.cache.new_pools(device="cpu", fill=0)
+
+    def check(self, workspace=None, err=None, **kw):
+        p = dict(kc=self.kc, kp=self.kp, vc=self.vc, vp=self.vp)
+        p.update(kw)
+        kvq._memory(self.cache, p["kc"], p["kp"], p["vc"], p["vp"], workspace, err)
+
+
+def test_pools_of_the_cache_are_taken():
+    p = Pools()
+    p.check()
+    p.check(workspace=torch.empty(64, dtype=torch.uint8), err=torch.zeros(1, dtype=torch.int32))
+    layers = torch.zeros((3, 6, 2, 16, 64), dtype=torch.uint8)
+    p.check(kc=layers[1], vc=layers[2])                          # a layer of a larger tensor
+    p.check(kc=torch.zeros((9, 2, 16, 64), dtype=torch.uint8))   # more pages than the cache names
+    p.check(kp=p.kp.view(6, 32), vc=p.vc.view(-1))               # the same bytes, fewer dimensions
+
+
+@pytest.mark.parametrize("name", ["kc", "kp", "vc", "vp"])
+def test_pools_that_would_be_misread_or_read_past_their_end_are_refused(name):
+    p = Pools()
+    t = getattr(p, name)
+    layers = torch.zeros((t.shape[0], 3, *t.shape[1:]), dtype=t.dtype)
+    for bad in (t[:5], t[:, :1].contiguous(), layers[:, 1], t.transpose(1, 2),
+                t.transpose(1, 2).contiguous(), t.float(), t.view(-1)[:-1],
+                torch.zeros((6, 4, *t.shape[2:]), dtype=t.dtype),
+                t.view(torch.int16) if name in ("kp", "vp") else t.view(torch.int32)):
+        with pytest.raises(ValueError):
+            p.check(**{name: bad})
+
+
+def test_workspace_and_error_words_that_do_not_fit_are_refused():
+    p = Pools()
+    for ws in (torch.empty((64, 2), dtype=torch.uint8)[:, 0], torch.empty((4, 8)).t()):
+        with pytest.raises(ValueError):
+            p.check(workspace=ws)
+    for err in (torch.zeros(1, dtype=torch.uint8), torch.zeros(1), torch.zeros(0, dtype=torch.int32),
+                torch.zeros(1, dtype=torch.int64)):
+        with pytest.raises(ValueError):
+            p.check(err=err)

@@ -216,3 +216,18 @@ def test_a_huge_cap_is_none(d, cap):
     if cap >= 1e30:
         assert torch.equal(p.run(cap=cap), p.run())
         assert torch.equal(scored(b, q, cap=cap), scored(b, q))
+
+
+def test_pools_that_do_not_fit_the_cache_are_refused_by_every_call():
+    b, q = batch([100, 60], seed=53)
+    ls, qs = b.i32(b.lens), b.i32(b.q_start)
+    calls = (lambda *p: kvq.paged_prefill_attn(b.cache, b.q, qs, 1, ls, 100, b.table, *p),
+             lambda *p: kvq.paged_decode_attn_scored(b.cache, q, ls, 100, b.table, *p),
+             lambda *p: kvq.shared_prefix_decode_attn(b.cache, q, 0, ls, 100, b.table, *p))
+    for call in calls:
+        call(b.kc, b.kp, b.vc, b.vp)
+        for p in ((b.kc[:-1], b.kp, b.vc, b.vp), (b.kc, b.kp[:, :1].contiguous(), b.vc, b.vp),
+                  (b.kc, b.kp, b.vc.transpose(1, 2), b.vp), (b.kc, b.kp, b.vc, b.vp.float())):
+            with pytest.raises(ValueError):
+                call(*p)
+    torch.cuda.synchronize()
