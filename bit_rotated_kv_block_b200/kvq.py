@@ -185,6 +185,14 @@ def _fit(cache, q, seqs, seq_lens, block_table, kc, kp, vc, vp, out, out_dtype, 
     return shape, dev
 
 
+def _i32(v, name):
+    """A size or position for the library (ctypes would keep its low 32 bits)."""
+    v = int(v)
+    if not -2147483648 <= v <= 2147483647:
+        raise ValueError(f"{name} does not fit 32 bits")
+    return v
+
+
 def _new(shape, dtype, q, stream):
     """Output or workspace of a call on ``stream``: allocated on it, so that its
     memory is neither taken from nor given to work that the call overlaps."""
@@ -361,7 +369,8 @@ def decode_step(cache, q, k_new, v_new, seq_lens, max_seq_len, block_table, k_co
 
 def prefill_workspace_bytes(cache, num_seqs, num_q_heads, num_tokens, max_q_len, max_seq_len):
     return int(lib().kvq_prefill_workspace_bytes(ctypes.byref(cache.desc), num_seqs, num_q_heads,
-                                                 num_tokens, max_q_len, max_seq_len))
+                                                 num_tokens, _i32(max_q_len, "max_q_len"),
+                                                 _i32(max_seq_len, "max_seq_len")))
 
 
 def paged_prefill_attn(cache, q, q_start, max_q_len, seq_lens, max_seq_len, block_table, k_codes,
@@ -388,8 +397,9 @@ def paged_prefill_attn(cache, q, q_start, max_q_len, seq_lens, max_seq_len, bloc
         workspace = _new(max(need, 16), torch.uint8, q, stream)
     st = lib().kvq_paged_prefill_attn(
         ctypes.byref(cache.desc), S, Hq, T, q.data_ptr(), q.stride(0) if T > 1 else Hq * d,
-        q_start.data_ptr(), int(max_q_len), seq_lens.data_ptr(), int(max_seq_len),
-        block_table.data_ptr(), int(block_table.shape[1]), float(sm_scale), _score(score, q, S, shape),
+        q_start.data_ptr(), _i32(max_q_len, "max_q_len"), seq_lens.data_ptr(),
+        _i32(max_seq_len, "max_seq_len"), block_table.data_ptr(), int(block_table.shape[1]),
+        float(sm_scale), _score(score, q, S, shape),
         k_codes.data_ptr(), k_params.data_ptr(), v_codes.data_ptr(), v_params.data_ptr(),
         out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _ptr(err), _stream(stream, dev))
     _check("kvq_paged_prefill_attn", st)
@@ -414,8 +424,8 @@ def paged_decode_attn_scored(cache, q, seq_lens, max_seq_len, block_table, k_cod
         need = decode_workspace_bytes(cache, S, Hq, max_seq_len)
         workspace = _new(max(need, 16), torch.uint8, q, stream)
     st = lib().kvq_paged_decode_attn_scored(
-        ctypes.byref(cache.desc), S, Hq, q.data_ptr(), seq_lens.data_ptr(), int(max_seq_len),
-        block_table.data_ptr(), int(block_table.shape[1]), float(sm_scale), _score(score, q, S, shape),
+        ctypes.byref(cache.desc), S, Hq, q.data_ptr(), seq_lens.data_ptr(),
+        _i32(max_seq_len, "max_seq_len"), block_table.data_ptr(), int(block_table.shape[1]), float(sm_scale), _score(score, q, S, shape),
         k_codes.data_ptr(), k_params.data_ptr(), v_codes.data_ptr(), v_params.data_ptr(),
         out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _ptr(err), _stream(stream, dev))
     _check("kvq_paged_decode_attn_scored", st)
@@ -424,7 +434,8 @@ def paged_decode_attn_scored(cache, q, seq_lens, max_seq_len, block_table, k_cod
 
 def shared_prefix_workspace_bytes(cache, num_seqs, num_q_heads, prefix_len, max_seq_len):
     return int(lib().kvq_shared_prefix_workspace_bytes(ctypes.byref(cache.desc), num_seqs,
-                                                       num_q_heads, prefix_len, max_seq_len))
+                                                       num_q_heads, _i32(prefix_len, "prefix_len"),
+                                                       _i32(max_seq_len, "max_seq_len")))
 
 
 def shared_prefix_decode_attn(cache, q, prefix_len, seq_lens, max_seq_len, block_table, k_codes,
@@ -447,8 +458,9 @@ def shared_prefix_decode_attn(cache, q, prefix_len, seq_lens, max_seq_len, block
         need = shared_prefix_workspace_bytes(cache, S, Hq, prefix_len, max_seq_len)
         workspace = _new(max(need, 16), torch.uint8, q, stream)
     st = lib().kvq_shared_prefix_decode_attn(
-        ctypes.byref(cache.desc), S, Hq, q.data_ptr(), int(prefix_len), seq_lens.data_ptr(),
-        int(max_seq_len), block_table.data_ptr(), int(block_table.shape[1]), float(sm_scale),
+        ctypes.byref(cache.desc), S, Hq, q.data_ptr(), _i32(prefix_len, "prefix_len"),
+        seq_lens.data_ptr(), _i32(max_seq_len, "max_seq_len"), block_table.data_ptr(),
+        int(block_table.shape[1]), float(sm_scale),
         _score(score, q, S, shape), k_codes.data_ptr(), k_params.data_ptr(), v_codes.data_ptr(),
         v_params.data_ptr(), out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _ptr(err),
         _stream(stream, dev))

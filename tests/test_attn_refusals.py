@@ -61,3 +61,36 @@ def test_workspace_and_error_words_that_do_not_fit_are_refused():
                 torch.zeros(1, dtype=torch.int64)):
         with pytest.raises(ValueError):
             p.check(err=err)
+
+
+@pytest.mark.parametrize("value", [2 ** 31, 2 ** 32, 2 ** 32 + 64, -2 ** 31 - 1])
+def test_sizes_beyond_32_bits_are_refused(monkeypatch, value):
+    # (ctypes would cut them to their low 32 bits)
+    p = Pools()
+    monkeypatch.setattr(kvq, "_fit", lambda cache, q, seqs, *a: (q.shape, 0))
+    monkeypatch.setattr(kvq, "_ints", lambda *a: None)
+    monkeypatch.setattr(kvq, "_stream", lambda *a: None)
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *a: 0
+    monkeypatch.setattr(kvq, "lib", lambda: Library())
+    q = torch.zeros((2, 4, 128), dtype=torch.float16)
+    lens, table = torch.zeros(2, dtype=torch.int32), torch.zeros((2, 4), dtype=torch.int32)
+    qs, pools = torch.zeros(3, dtype=torch.int32), (p.kc, p.kp, p.vc, p.vp)
+    ws = torch.zeros(64, dtype=torch.uint8)
+    good = lambda v=16: (
+        lambda: kvq.paged_prefill_attn(p.cache, q, qs, v, lens, 64, table, *pools, workspace=ws),
+        lambda: kvq.paged_prefill_attn(p.cache, q, qs, 4, lens, v, table, *pools, workspace=ws),
+        lambda: kvq.paged_decode_attn_scored(p.cache, q, lens, v, table, *pools, workspace=ws),
+        lambda: kvq.shared_prefix_decode_attn(p.cache, q, v, lens, 64, table, *pools, workspace=ws),
+        lambda: kvq.shared_prefix_decode_attn(p.cache, q, 16, lens, v, table, *pools, workspace=ws),
+        lambda: kvq.prefill_workspace_bytes(p.cache, 2, 4, 2, v, 64),
+        lambda: kvq.prefill_workspace_bytes(p.cache, 2, 4, 2, 4, v),
+        lambda: kvq.shared_prefix_workspace_bytes(p.cache, 2, 4, v, 64),
+        lambda: kvq.shared_prefix_workspace_bytes(p.cache, 2, 4, 16, v))
+    for call in good():
+        call()
+    for call in good(value):
+        with pytest.raises(ValueError):
+            call()
