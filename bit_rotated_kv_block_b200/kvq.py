@@ -425,7 +425,8 @@ def paged_decode_attn_scored(cache, q, seq_lens, max_seq_len, block_table, k_cod
         workspace = _new(max(need, 16), torch.uint8, q, stream)
     st = lib().kvq_paged_decode_attn_scored(
         ctypes.byref(cache.desc), S, Hq, q.data_ptr(), seq_lens.data_ptr(),
-        _i32(max_seq_len, "max_seq_len"), block_table.data_ptr(), int(block_table.shape[1]), float(sm_scale), _score(score, q, S, shape),
+        _i32(max_seq_len, "max_seq_len"), block_table.data_ptr(), int(block_table.shape[1]),
+        float(sm_scale), _score(score, q, S, shape),
         k_codes.data_ptr(), k_params.data_ptr(), v_codes.data_ptr(), v_params.data_ptr(),
         out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _ptr(err), _stream(stream, dev))
     _check("kvq_paged_decode_attn_scored", st)
