@@ -231,3 +231,14 @@ def test_pools_that_do_not_fit_the_cache_are_refused_by_every_call():
             with pytest.raises(ValueError):
                 call(*p)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_rows_of_the_valid_sequence_beside_a_bad_range_when_keys_are_split(d):
+    b = Batch([4000, 2500], [5, 3], d=d, tail=9, seed=11)
+    b.q_start = [2, 7, 60]           # the second sequence's is no range of the rows
+    out = b.run()
+    assert int(b.err.item()) == kvq.ERRF_SEQ
+    b.qn = [5, 0]
+    b.check(out)
+    assert bool((out[:2] == 7.0).all()) and bool((out[7:] == 7.0).all())
