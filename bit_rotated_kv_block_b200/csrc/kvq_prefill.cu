@@ -25,12 +25,12 @@
 //    tensor memory. S has two buffers, so one tile's softmax runs under the
 //    products of its neighbours.
 //
-// What bounds it (d = 128, one B200): a key tile of 128 takes 1.41 us, 2700
-// cycles at 1.92 GHz, of which the softmax warps' own chain (read S, scale,
-// maximum, exponentials, write P) is the whole: 24 products of 74 cycles take
-// 1776 (2130 with their hand-overs and no softmax at all), the exponentials
-// 1024 of the special-function pipe, all instructions 1290 issue slots per
-// scheduler. A CTA's first S comes 6 us after its start and its end 3 us after
+// What bounds it (d = 128, one B200): a key tile of 128 takes 1.40 us, 2700
+// cycles at 1.92 GHz (2.7 us with a cap, 2.5 us with a bias alone), of which
+// the softmax warps' own chain (read S, scale, maximum, exponentials, write P)
+// is the whole: 24 products of 74 cycles take 1776 (2130 with their hand-overs
+// and no softmax at all), the exponentials 1024 of the special-function pipe,
+// all instructions 1290 issue slots per scheduler. A CTA's first S comes 6 us after its start and its end 3 us after
 // the last product; at 4096 tokens that is a third of the time. Measured and
 // not kept: one CTA per SM walking over items with the next query copied
 // ahead (prompt 233 -> 234 us, few rows 25 -> 30 us), a tile per softmax
@@ -1352,8 +1352,9 @@ static PrefillPlan plan_rows(int D, int H, int64_t nseq, int64_t rows_per_seq, i
   if (pl.mtiles < 1) pl.mtiles = 1;
   // at most half a tile's rows: the free lanes take the weights' lower parts and
   // the rows lie on all four schedulers. 8 sequences x 20 rows: 35.0 -> 34.2 us,
-  // error 3.1e-4 -> 2.9e-4; a 512-token prefix of 16 rows: 16.3 -> 17.1 us (two
-  // tiles per CTA, each with a second store), 3.0e-4 -> 2.7e-4
+  // error 3.1e-4 -> 2.9e-4 (35.5 us since P V completes before the next S); a
+  // 512-token prefix of 16 rows: 16.3 -> 17.1 us (two tiles per CTA, each with a
+  // second store), 3.0e-4 -> 2.7e-4
   pl.pair = rows_per_seq <= rt / 2;
   const int64_t ctas = nseq * H * pl.mtiles;
   const int64_t tiles = (max_keys + kt - 1) / kt;

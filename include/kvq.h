@@ -400,8 +400,9 @@ int kvq_paged_decode_attn_scored(const kvq_cache_desc* desc, int32_t num_seqs,
  * kvq_shared_prefix_decode_attn -- decode attention for a batch whose
  * sequences begin with the same prefix_len tokens: the prefix's pages are
  * read once per KV head for the whole batch instead of once per sequence.
- * The result is that of kvq_paged_decode_attn_scored on the same cache,
- * rounded to binary16.
+ * The result is what kvq_paged_decode_attn_scored computes on the same cache,
+ * in binary16 and, over the prefix's positions, with the operand roundings of
+ * kvq_paged_prefill_attn (accuracy below).
  *
  *  prefix_len   P0 >= 0, a host value: positions [0, P0) of every sequence
  *               hold the same tokens; their pages are taken from row 0 of
@@ -418,7 +419,8 @@ int kvq_paged_decode_attn_scored(const kvq_cache_desc* desc, int32_t num_seqs,
  *  workspace    >= kvq_shared_prefix_workspace_bytes(...) bytes, 16-byte
  *               aligned; no initialisation.
  * Supported: KVQ_FMT_INT4 and the geometries of kvq_paged_decode_attn. The
- * prefix part has the accuracy of kvq_paged_prefill_attn.
+ * prefix part has the accuracy of kvq_paged_prefill_attn (weights and values
+ * rounded to binary16 once each), the own part that of the scored decode.
  */
 size_t kvq_shared_prefix_workspace_bytes(const kvq_cache_desc* desc, int32_t num_seqs,
                                          int32_t num_q_heads, int32_t prefix_len,
