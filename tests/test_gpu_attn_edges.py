@@ -242,3 +242,70 @@ def test_rows_of_the_valid_sequence_beside_a_bad_range_when_keys_are_split(d):
     b.qn = [5, 0]
     b.check(out)
     assert bool((out[:2] == 7.0).all()) and bool((out[7:] == 7.0).all())
+
+
+@pytest.mark.parametrize("word", [0x00007BFF, 0x7BFF7BFF, 0x7BFF0000, 0xFBFF7BFF - 2 ** 32, 0x7BFFFBFF],
+                         ids=hex)
+@pytest.mark.parametrize("d,lens,qn", [(128, [300], [200]), (256, [300], [200]), (128, [700], [9]),
+                                       (128, [2500], [40])], ids=str)
+def test_the_largest_finite_scales_and_minima(d, lens, qn, word):
+    # (scale, minimum) of +-65504 and 0, one channel with code 15: values up to
+    # 1.05e6. Zero queries weigh the seen tokens alike, so the results stay finite.
+    b = Batch(lens, qn, d=d, H=2, G=4, block=d, seed=54)
+    b.qbuf.zero_()
+    at = 70
+    page, slot = int(b.table[0, at // 16]), at % 16
+    b.vp[page, :, slot] = word
+    b.vc[page, :, slot] = 0
+    b.vc[page, :, slot, 5] = 0x0F
+    for kw in (dict(), dict(cap=20.0, window=250)):
+        out = b.run(**kw)
+        assert bool(out.isfinite().all())
+        check_prompt(b, out, **kw)
+        q = b.q[-1:].contiguous()
+        check_scored(b, scored(b, q, **kw), q, 1, **kw)
+    assert int(b.err.item()) == 0
+
+
+def test_calls_on_two_streams_at_once():
+    b, q = batch([900, 700, 811], seed=55)
+    share(b, 640)
+    p = Batch([500, 210], [30, 210], seed=56)
+    want = shared(b, q, 640, cap=20.0), scored(b, q, window=300), p.run(cap=20.0)
+    lens, plens, qs = b.i32(b.lens), p.i32(p.lens), p.i32(p.q_start)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = []
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for st in streams:       # each call's output and workspace are its own
+            pb, pp = (b.kc, b.kp, b.vc, b.vp), (p.kc, p.kp, p.vc, p.vp)
+            outs.append((kvq.shared_prefix_decode_attn(b.cache, q, 640, lens, 900, b.table, *pb,
+                                                       score=kvq.Score(20.0), stream=st),
+                         kvq.paged_decode_attn_scored(b.cache, q, lens, 900, b.table, *pb,
+                                                      score=kvq.Score(window=300), stream=st),
+                         kvq.paged_prefill_attn(p.cache, p.q, qs, 210, plens, 500, p.table, *pp,
+                                                score=kvq.Score(20.0), stream=st)))
+    torch.cuda.synchronize()
+    for o in outs:
+        assert all(torch.equal(x, y) for x, y in zip(o, want))
+
+
+def test_many_sequences_with_few_tokens():
+    S = 1500
+    b = Batch([65 + i % 40 for i in range(S)], [1 + i % 3 for i in range(S)], H=1, G=4, seed=57)
+    out = b.run()
+    pick = list(range(0, S, 97))
+    for s in pick:
+        n = b.qn[s]
+        ref, A, Sz, top = rows_of(b, s, b.q[b.q_start[s]:b.q_start[s] + n],
+                                  torch.arange(b.lens[s] - n, b.lens[s], device="cuda"))
+        off = (out[b.q_start[s]:b.q_start[s] + n].double() - ref).norm(dim=-1)
+        assert bool((off <= half_tolerance(ref, A, Sz, b.lens[s], top)).all())
+    share(b, 64)
+    q = torch.randn((S, 4, 128), generator=torch.Generator().manual_seed(58)).half().cuda()
+    got = shared(b, q, 64)
+    for s in pick:
+        ref, A, Sz, top = rows_of(b, s, q[s:s + 1], torch.tensor([b.lens[s] - 1], device="cuda"))
+        off = (got[s].double() - ref[0]).norm(dim=-1)
+        assert bool((off <= half_tolerance(ref, A, Sz, b.lens[s], top)[0]).all())
+    assert int(b.err.item()) == 0
